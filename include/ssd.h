@@ -295,6 +295,134 @@ ssd_status ssd_forward_planned(const ssd_problem *problem, const ssd_launch_plan
 ssd_status ssd_workspace_layout(const ssd_problem *problem, size_t *off_G2, size_t *off_dtT,
                                 size_t *off_S);
 
+/* ---------------------------------------------------------------------------
+ * The operators around the forward: what a block runs right before and after ssd_forward
+ * (ssd_step), and the selective scan that takes its place in blocks whose decay differs
+ * per channel and state.  The conventions above hold (host validation before any launch,
+ * no allocation, no synchronisation, capture into a HIP graph), with these additions:
+ *   - inputs may be column slices of a wider row-major array: a *_pitch is the number of
+ *     elements from one token (row) to the next, 0 standing for dense rows; the batches
+ *     follow each other after seqlen tokens.  Outputs and states are dense.
+ *   - `lengths` (device, int32 [b], NULL: every sequence has seqlen tokens) gives the
+ *     tokens of each sequence of a padded batch, each taken as at least 0 and at most
+ *     seqlen.  Rows behind a sequence's length are not read and their outputs are left as
+ *     they were; the final state is the one after the sequence's own last token (with
+ *     length 0 the initial state, or zeros).
+ *   - element alignment is enough for x, z, dt, y, the conv states and the residual
+ *     stream (rows on 16 bytes run faster); stricter cases are named per entry point.
+ *   - exponentials, sums, states and norms are fp32; each output is rounded once.
+ * ------------------------------------------------------------------------- */
+
+/* Short causal depthwise convolution.  For every channel c, with K = width taps,
+ *     v[b,t,c] = bias[c] + sum_{k < K} weight[c,k] x[b, t - K + 1 + k, c]
+ *     out      = v / (1 + exp(-v)) when silu, else v
+ * where tokens before the first come from the conv state: the last K - 1 inputs, oldest
+ * first (NULL: zeros).  The outputs are up to three dense arrays that take the channels in
+ * turn (split: for a block's x, B and C columns, ready for ssd_forward), y_i [b, L,
+ * split[i]]; a split of 0 has no array. */
+typedef struct {
+    int64_t batch, seqlen, channels;
+    int64_t x_pitch;          /* 0: channels */
+    int64_t split[3];         /* split[0] > 0, no gap, sum = channels */
+    int32_t width;            /* 2, 3 or 4 */
+    int32_t silu;             /* 0 or 1 */
+    int32_t dtype;            /* an ssd_dtype value: x, y, state */
+} ssd_conv_problem;
+
+/* Host-only checks: dimensions positive, split and pitch as described (a pitch is 0 or at
+ * least the row's width) else SSD_ERR_BAD_SHAPE; dtype, width and flags in their sets,
+ * seqlen <= 2^30, channels <= 2^24, batch * seqlen <= 2^31, pitch <= 2^28 and
+ * ceil(channels / 256) * ceil(seqlen / 8) * batch < 2^24 else SSD_ERR_UNSUPPORTED. */
+ssd_status ssd_conv_validate(const ssd_conv_problem *problem);
+
+/* The convolution over whole prompts.  x [b,L,channels] and y in `dtype`; weight
+ * [channels, width] and bias [channels] (may be NULL) float32 on 16 bytes
+ * (SSD_ERR_MISALIGNED otherwise); state0 [b, width-1, channels] in `dtype` or NULL;
+ * stateT of the same shape or NULL (not wanted); state0 and stateT may be one buffer. */
+ssd_status ssd_conv(const ssd_conv_problem *problem, const void *x, const float *weight,
+                    const float *bias, const void *state0, const int32_t *lengths, void *y0,
+                    void *y1, void *y2, void *stateT, void *stream);
+
+/* One token per sequence (problem->seqlen must be 1, else SSD_ERR_BAD_SHAPE): x [b,
+ * channels] with x_pitch from one sequence to the next, y_i [b, split[i]]; state [b,
+ * width-1, channels] is shifted by one token in place.  Continues ssd_conv's stateT. */
+ssd_status ssd_conv_step(const ssd_conv_problem *problem, const void *x, const float *weight,
+                         const float *bias, void *state, void *y0, void *y1, void *y2,
+                         void *stream);
+
+/* Selective state space scan.  For every channel c, of group g = c / (channels / ngroups),
+ * and state n,
+ *     d_t[c]   = dt[b,t,c] + dt_bias[c], and log(1 + exp(d)) of that when softplus
+ *     h_t[c,n] = exp(d_t[c] A[c,n]) h_{t-1}[c,n] + d_t[c] x[b,t,c] B[b,t,g,n]
+ *     y[b,t,c] = (sum_n C[b,t,g,n] h_t[c,n] + D[c] x[b,t,c]) z / (1 + exp(-z))
+ * with the last factor (the gate) only where z is given. */
+typedef struct {
+    int64_t batch, seqlen, channels, ngroups, dstate;
+    int64_t x_pitch, dt_pitch, z_pitch;   /* 0: channels */
+    int64_t B_pitch, C_pitch;             /* 0: ngroups * dstate */
+    int32_t softplus;                     /* 0 or 1 */
+    int32_t dtype;                        /* x, dt, B, C, z, y */
+} ssd_scan_problem;
+
+/* Host-only checks: dimensions positive, channels divisible by ngroups, a pitch 0 or at
+ * least the row's width, else SSD_ERR_BAD_SHAPE; dstate a multiple of 8 up to 64, dtype and
+ * flag in their sets, seqlen <= 2^30, channels <= 2^24, batch * seqlen <= 2^31, pitches <=
+ * 2^28, batch * channels <= 2^31 / dstate and ngroups * ceil(channels / ngroups / 64) *
+ * batch < 2^20 else SSD_ERR_UNSUPPORTED. */
+ssd_status ssd_scan_validate(const ssd_scan_problem *problem);
+
+/* Bytes of device workspace ssd_scan needs; 0 if `problem` is not valid.  Host-only. */
+size_t ssd_scan_workspace_bytes(const ssd_scan_problem *problem);
+
+/* The scan over whole prompts.  x, dt, z, y [b,L,channels] and B, C [b,L,ngroups,dstate] in
+ * `dtype`; A [channels, dstate], D and dt_bias [channels] float32; h0, hT [b, channels,
+ * dstate] float32, which may be one buffer.  D, z, dt_bias, h0, lengths and hT may be NULL.
+ * A, h0, hT and the workspace start on 16 bytes, B and C on 4 bytes with even pitches for
+ * SSD_BF16, else SSD_ERR_MISALIGNED. */
+ssd_status ssd_scan(const ssd_scan_problem *problem, const void *x, const void *dt,
+                    const float *A, const void *B, const void *C, const float *D, const void *z,
+                    const float *dt_bias, const float *h0, const int32_t *lengths, void *y,
+                    float *hT, void *workspace, size_t workspace_bytes, void *stream);
+
+/* One token per sequence (problem->seqlen must be 1, else SSD_ERR_BAD_SHAPE): x, dt, z, y
+ * [b, channels] and B, C [b, ngroups, dstate], pitches from one sequence to the next; h [b,
+ * channels, dstate] is updated in place.  Alignment as for ssd_scan.  Continues ssd_scan's
+ * hT. */
+ssd_status ssd_scan_step(const ssd_scan_problem *problem, const void *x, const void *dt,
+                         const float *A, const void *B, const void *C, const float *D,
+                         const void *z, const float *dt_bias, float *h, void *y, void *stream);
+
+/* RMS norm before or after a block, by row and group of channels / ngroups channels, with
+ * the block's gate and the scaled residual addition:
+ *     v = x;                   gate first (gate_after 0, z given): v *= z / (1 + exp(-z))
+ *     residual given:          v = residual + scale v
+ *     residual_out[r,c] = v    rounded to the residual's type (the norm takes the sum
+ *                              itself, not the rounded one)
+ *     y[r,c] = v / sqrt(mean_group(v^2) + eps) weight[c]
+ *                              gate after (gate_after 1, z given): y *= z / (1 + exp(-z)) */
+typedef struct {
+    int64_t rows, channels, ngroups;
+    int64_t x_pitch, z_pitch;     /* 0: channels */
+    float eps;                    /* > 0, finite */
+    float scale;                  /* finite; read with a residual only */
+    int32_t gate_after;           /* 0 or 1 */
+    int32_t dtype;                /* x, z, y */
+    int32_t residual_dtype;       /* residual, residual_out: SSD_F32 or `dtype` */
+} ssd_norm_problem;
+
+/* Host-only checks: dimensions positive, channels divisible by ngroups, pitches as above
+ * else SSD_ERR_BAD_SHAPE; dtypes, flag, eps and scale in their sets, channels <= 2^24,
+ * pitches <= 2^28, rows <= 2^31 and rows * ngroups < 2^24 else SSD_ERR_UNSUPPORTED. */
+ssd_status ssd_norm_validate(const ssd_norm_problem *problem);
+
+/* x, z, y [rows, channels]; z may be NULL (no gate); residual [rows, channels] may be NULL
+ * (no addition; residual_out must then be NULL too), residual_out may be NULL (not wanted)
+ * and may be the residual's own buffer; weight [channels] float32 on 16 bytes
+ * (SSD_ERR_MISALIGNED otherwise). */
+ssd_status ssd_norm(const ssd_norm_problem *problem, const void *x, const void *z,
+                    const void *residual, const float *weight, void *y, void *residual_out,
+                    void *stream);
+
 /* Static text for a status code. */
 const char *ssd_status_string(ssd_status status);
 

@@ -13,7 +13,9 @@ LIBRARY = os.path.join(PKG, "libssd.so")
 SOURCES = [os.path.join(CSRC, "ssd_kernels.hip"), os.path.join(CSRC, "ssd_bf16.hip"),
            os.path.join(CSRC, "ssd_step.hip"), os.path.join(CSRC, "ssd_noalloc.hip"),
            os.path.join(CSRC, "ssd_small.hip"),
-           os.path.join(CSRC, "ssd_api.cpp")]
+           os.path.join(CSRC, "ssd_conv.hip"), os.path.join(CSRC, "ssd_scan.hip"),
+           os.path.join(CSRC, "ssd_norm.hip"),
+           os.path.join(CSRC, "ssd_api.cpp"), os.path.join(CSRC, "ssd_block_api.cpp")]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",

@@ -1,0 +1,232 @@
+// ssd_block_api.cpp -- C entry points of the operators around the forward: the short causal
+// convolution, the selective scan and the block norms.  Host-side validation only; the
+// kernels are in ssd_conv.hip, ssd_scan.hip and ssd_norm.hip.
+#include "../../include/ssd.h"
+
+#include <hip/hip_runtime.h>
+
+#include <initializer_list>
+
+#include "ssd_launch.h"
+
+namespace {
+
+constexpr int64_t kMaxPitch = int64_t(1) << 28;
+constexpr int64_t kMaxTokens = int64_t(1) << 30;
+constexpr int64_t kMaxRows = int64_t(1) << 31;       // batch * seqlen
+constexpr int64_t kMaxChannels = int64_t(1) << 24;
+// Workgroups of 256 threads: the dispatch grid counts work-items in 32 bits.
+constexpr int64_t kMaxGrid = int64_t(1) << 24;
+
+bool on_bytes(size_t n, std::initializer_list<const void *> ptrs)
+{
+    for (const void *p : ptrs)
+        if ((reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0) return false;
+    return true;
+}
+
+bool is_dtype(int32_t d) { return d == SSD_F32 || d == SSD_BF16; }
+bool is_flag(int32_t f) { return f == 0 || f == 1; }
+// 0 (dense) or at least the row's width
+bool pitch_fits(int64_t pitch, int64_t width) { return pitch == 0 || pitch >= width; }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+bool finite(float v) { return v - v == 0.0f; }
+
+// batch and seqlen (both positive) within the index limits
+bool tokens_fit(int64_t batch, int64_t seqlen)
+{
+    return seqlen <= kMaxTokens && batch <= kMaxRows / seqlen;
+}
+
+ssd_status check_conv(const ssd_conv_problem *p)
+{
+    if (p == nullptr) return SSD_ERR_NULL_ARG;
+    if (p->batch <= 0 || p->seqlen <= 0 || p->channels <= 0) return SSD_ERR_BAD_SHAPE;
+    const int64_t *w = p->split;
+    if (w[0] <= 0 || w[1] < 0 || w[2] < 0 || (w[1] == 0 && w[2] > 0)) return SSD_ERR_BAD_SHAPE;
+    if (w[0] > p->channels || w[1] > p->channels || w[2] > p->channels - w[0] ||
+        w[0] + w[1] + w[2] != p->channels)
+        return SSD_ERR_BAD_SHAPE;
+    if (!pitch_fits(p->x_pitch, p->channels)) return SSD_ERR_BAD_SHAPE;
+    if (!is_dtype(p->dtype) || !is_flag(p->silu) || p->width < 2 || p->width > 4)
+        return SSD_ERR_UNSUPPORTED;
+    if (p->channels > kMaxChannels || p->x_pitch > kMaxPitch || !tokens_fit(p->batch, p->seqlen))
+        return SSD_ERR_UNSUPPORTED;
+    const int64_t tiles = ceil_div(p->channels, 256) * ceil_div(p->seqlen, 8);
+    if (p->batch > (kMaxGrid - 1) / tiles) return SSD_ERR_UNSUPPORTED;
+    return SSD_OK;
+}
+
+ssd::ConvShape conv_shape(const ssd_conv_problem *p)
+{
+    ssd::ConvShape s;
+    s.b = p->batch; s.L = p->seqlen; s.C = p->channels;
+    s.pitch = p->x_pitch ? p->x_pitch : p->channels;
+    s.w0 = p->split[0]; s.w1 = p->split[1]; s.w2 = p->split[2];
+    s.K = p->width;
+    s.silu = p->silu != 0;
+    s.bf16 = p->dtype == SSD_BF16;
+    return s;
+}
+
+ssd_status check_scan(const ssd_scan_problem *p)
+{
+    if (p == nullptr) return SSD_ERR_NULL_ARG;
+    if (p->batch <= 0 || p->seqlen <= 0 || p->channels <= 0 || p->ngroups <= 0 || p->dstate <= 0)
+        return SSD_ERR_BAD_SHAPE;
+    if (p->channels % p->ngroups != 0) return SSD_ERR_BAD_SHAPE;
+    if (p->dstate % 8 != 0 || p->dstate > 64 || p->channels > kMaxChannels)
+        return SSD_ERR_UNSUPPORTED;
+    const int64_t gn = p->ngroups * p->dstate;   // at most channels * 64
+    if (!pitch_fits(p->x_pitch, p->channels) || !pitch_fits(p->dt_pitch, p->channels) ||
+        !pitch_fits(p->z_pitch, p->channels) || !pitch_fits(p->B_pitch, gn) ||
+        !pitch_fits(p->C_pitch, gn))
+        return SSD_ERR_BAD_SHAPE;
+    if (!is_dtype(p->dtype) || !is_flag(p->softplus)) return SSD_ERR_UNSUPPORTED;
+    for (int64_t pitch : {p->x_pitch, p->dt_pitch, p->z_pitch, p->B_pitch, p->C_pitch, gn})
+        if (pitch > kMaxPitch) return SSD_ERR_UNSUPPORTED;
+    if (!tokens_fit(p->batch, p->seqlen)) return SSD_ERR_UNSUPPORTED;
+    if (p->batch > kMaxRows / p->dstate / p->channels) return SSD_ERR_UNSUPPORTED;
+    const int64_t tiles = ceil_div(p->channels / p->ngroups, 64) * p->ngroups;
+    if (p->batch > ((int64_t(1) << 20) - 1) / tiles) return SSD_ERR_UNSUPPORTED;
+    return SSD_OK;
+}
+
+ssd::ScanShape scan_shape(const ssd_scan_problem *p)
+{
+    ssd::ScanShape s;
+    s.b = p->batch; s.L = p->seqlen; s.C = p->channels; s.G = p->ngroups; s.N = p->dstate;
+    s.xp = p->x_pitch ? p->x_pitch : p->channels;
+    s.dtp = p->dt_pitch ? p->dt_pitch : p->channels;
+    s.zp = p->z_pitch ? p->z_pitch : p->channels;
+    s.Bp = p->B_pitch ? p->B_pitch : p->ngroups * p->dstate;
+    s.Cp = p->C_pitch ? p->C_pitch : p->ngroups * p->dstate;
+    s.softplus = p->softplus != 0;
+    s.bf16 = p->dtype == SSD_BF16;
+    return s;
+}
+
+// B and C rows are read by scalar loads, which take whole dwords.
+ssd_status check_scan_pointers(const ssd_scan_problem *p, const void *A, const void *B,
+                               const void *C, std::initializer_list<const void *> states)
+{
+    if (!on_bytes(16, {A}) || !on_bytes(16, states) || !on_bytes(4, {B, C}))
+        return SSD_ERR_MISALIGNED;
+    if (p->dtype == SSD_BF16 && (p->B_pitch % 2 != 0 || p->C_pitch % 2 != 0))
+        return SSD_ERR_MISALIGNED;
+    return SSD_OK;
+}
+
+ssd_status check_norm(const ssd_norm_problem *p)
+{
+    if (p == nullptr) return SSD_ERR_NULL_ARG;
+    if (p->rows <= 0 || p->channels <= 0 || p->ngroups <= 0) return SSD_ERR_BAD_SHAPE;
+    if (p->channels % p->ngroups != 0) return SSD_ERR_BAD_SHAPE;
+    if (!pitch_fits(p->x_pitch, p->channels) || !pitch_fits(p->z_pitch, p->channels))
+        return SSD_ERR_BAD_SHAPE;
+    if (!is_dtype(p->dtype) || !is_flag(p->gate_after)) return SSD_ERR_UNSUPPORTED;
+    if (p->residual_dtype != SSD_F32 && p->residual_dtype != p->dtype) return SSD_ERR_UNSUPPORTED;
+    if (!finite(p->eps) || !(p->eps > 0.0f) || !finite(p->scale)) return SSD_ERR_UNSUPPORTED;
+    if (p->channels > kMaxChannels || p->x_pitch > kMaxPitch || p->z_pitch > kMaxPitch ||
+        p->rows > kMaxRows || p->rows > (kMaxGrid - 1) / p->ngroups)
+        return SSD_ERR_UNSUPPORTED;
+    return SSD_OK;
+}
+
+ssd_status status_of(hipError_t e) { return ssd_status(ssd::hip_status(e)); }
+
+}  // namespace
+
+extern "C" {
+
+ssd_status ssd_conv_validate(const ssd_conv_problem *problem) { return check_conv(problem); }
+
+ssd_status ssd_conv(const ssd_conv_problem *problem, const void *x, const float *weight,
+                    const float *bias, const void *state0, const int32_t *lengths, void *y0,
+                    void *y1, void *y2, void *stateT, void *stream)
+{
+    const ssd_status st = check_conv(problem);
+    if (st != SSD_OK) return st;
+    if (!x || !weight || !y0 || (problem->split[1] > 0 && !y1) || (problem->split[2] > 0 && !y2))
+        return SSD_ERR_NULL_ARG;
+    if (!on_bytes(16, {weight, bias})) return SSD_ERR_MISALIGNED;
+    return status_of(ssd::launch_conv(conv_shape(problem), x, weight, bias, state0, lengths, y0,
+                                      y1, y2, stateT, (hipStream_t)stream));
+}
+
+ssd_status ssd_conv_step(const ssd_conv_problem *problem, const void *x, const float *weight,
+                         const float *bias, void *state, void *y0, void *y1, void *y2,
+                         void *stream)
+{
+    const ssd_status st = check_conv(problem);
+    if (st != SSD_OK) return st;
+    if (problem->seqlen != 1) return SSD_ERR_BAD_SHAPE;
+    if (!x || !weight || !state || !y0 || (problem->split[1] > 0 && !y1) ||
+        (problem->split[2] > 0 && !y2))
+        return SSD_ERR_NULL_ARG;
+    if (!on_bytes(16, {weight, bias})) return SSD_ERR_MISALIGNED;
+    return status_of(ssd::launch_conv_step(conv_shape(problem), x, weight, bias, state, y0, y1,
+                                           y2, (hipStream_t)stream));
+}
+
+ssd_status ssd_scan_validate(const ssd_scan_problem *problem) { return check_scan(problem); }
+
+size_t ssd_scan_workspace_bytes(const ssd_scan_problem *problem)
+{
+    return check_scan(problem) == SSD_OK ? ssd::scan_workspace_bytes(scan_shape(problem)) : 0;
+}
+
+ssd_status ssd_scan(const ssd_scan_problem *problem, const void *x, const void *dt,
+                    const float *A, const void *B, const void *C, const float *D, const void *z,
+                    const float *dt_bias, const float *h0, const int32_t *lengths, void *y,
+                    float *hT, void *workspace, size_t workspace_bytes, void *stream)
+{
+    ssd_status st = check_scan(problem);
+    if (st != SSD_OK) return st;
+    if (!x || !dt || !A || !B || !C || !y) return SSD_ERR_NULL_ARG;
+    const ssd::ScanShape s = scan_shape(problem);
+    if (workspace == nullptr || workspace_bytes < ssd::scan_workspace_bytes(s))
+        return SSD_ERR_WORKSPACE;
+    st = check_scan_pointers(problem, A, B, C, {h0, hT, workspace});
+    if (st != SSD_OK) return st;
+    const ssd::ScanArgs a = {x, dt, A, B, C, D, z, dt_bias, h0, lengths, y, hT, workspace};
+    return status_of(ssd::launch_scan(s, a, (hipStream_t)stream));
+}
+
+ssd_status ssd_scan_step(const ssd_scan_problem *problem, const void *x, const void *dt,
+                         const float *A, const void *B, const void *C, const float *D,
+                         const void *z, const float *dt_bias, float *h, void *y, void *stream)
+{
+    ssd_status st = check_scan(problem);
+    if (st != SSD_OK) return st;
+    if (problem->seqlen != 1) return SSD_ERR_BAD_SHAPE;
+    if (!x || !dt || !A || !B || !C || !h || !y) return SSD_ERR_NULL_ARG;
+    st = check_scan_pointers(problem, A, B, C, {h});
+    if (st != SSD_OK) return st;
+    const ssd::ScanArgs a = {x, dt, A, B, C, D, z, dt_bias, nullptr, nullptr, y, nullptr, nullptr};
+    return status_of(ssd::launch_scan_step(scan_shape(problem), a, h, (hipStream_t)stream));
+}
+
+ssd_status ssd_norm_validate(const ssd_norm_problem *problem) { return check_norm(problem); }
+
+ssd_status ssd_norm(const ssd_norm_problem *problem, const void *x, const void *z,
+                    const void *residual, const float *weight, void *y, void *residual_out,
+                    void *stream)
+{
+    const ssd_status st = check_norm(problem);
+    if (st != SSD_OK) return st;
+    if (!x || !weight || !y || (residual_out && !residual)) return SSD_ERR_NULL_ARG;
+    if (!on_bytes(16, {weight})) return SSD_ERR_MISALIGNED;
+    ssd::NormShape s;
+    s.rows = problem->rows; s.C = problem->channels; s.G = problem->ngroups;
+    s.xp = problem->x_pitch ? problem->x_pitch : problem->channels;
+    s.zp = problem->z_pitch ? problem->z_pitch : problem->channels;
+    s.eps = problem->eps; s.scale = problem->scale;
+    s.gate_after = problem->gate_after != 0;
+    s.bf16 = problem->dtype == SSD_BF16;
+    s.res_bf16 = problem->residual_dtype == SSD_BF16;
+    return status_of(ssd::launch_norm(s, x, z, residual, weight, y, residual_out,
+                                      (hipStream_t)stream));
+}
+
+}  // extern "C"

@@ -108,6 +108,61 @@ hipError_t launch_decode_step(const Shape &s, const void *x, const void *dt, con
                               const void *B, const void *C, const float *D, float *h, void *y,
                               hipStream_t st);
 
+// ---------------------------------------------------------------------------
+// The operators around the forward (ssd_conv.hip, ssd_scan.hip, ssd_norm.hip; C entries in
+// ssd_block_api.cpp).  Pitches are elements from one token (row) to the next.
+// ---------------------------------------------------------------------------
+struct ConvShape {
+    int64_t b, L, C, pitch;
+    int64_t w0, w1, w2;     // channels of the three outputs, w0 + w1 + w2 = C
+    int K;
+    bool silu, bf16;
+};
+// lengths, bias, state0 and stateT may be NULL; y1 / y2 are NULL where w1 / w2 is 0
+hipError_t launch_conv(const ConvShape &s, const void *x, const float *w, const float *bias,
+                       const void *state0, const int32_t *lengths, void *y0, void *y1, void *y2,
+                       void *stateT, hipStream_t st);
+// One token per sequence (s.L = 1), state shifted in place.
+hipError_t launch_conv_step(const ConvShape &s, const void *x, const float *w, const float *bias,
+                            void *state, void *y0, void *y1, void *y2, hipStream_t st);
+// Workgroups of either launch (256 threads each), for the grid check.
+int64_t conv_workgroups(const ConvShape &s);
+
+struct ScanShape {
+    int64_t b, L, C, G, N;
+    int64_t xp, dtp, zp, Bp, Cp;
+    bool softplus, bf16;
+};
+struct ScanArgs {
+    const void *x, *dt;
+    const float *A;
+    const void *B, *C;
+    const float *D;          // may be NULL: no skip
+    const void *z;           // may be NULL: no gate
+    const float *dt_bias;    // may be NULL
+    const float *h0;         // may be NULL: zero
+    const int32_t *lengths;  // may be NULL: all L
+    void *y;
+    float *hT;               // may be NULL
+    void *ws;
+};
+size_t scan_workspace_bytes(const ScanShape &s);
+// Workgroups of the largest launch, for the grid check.
+int64_t scan_workgroups(const ScanShape &s);
+hipError_t launch_scan(const ScanShape &s, const ScanArgs &a, hipStream_t st);
+// One token per sequence (s.L = 1), h [b, C, N] updated in place.
+hipError_t launch_scan_step(const ScanShape &s, const ScanArgs &a, float *h, hipStream_t st);
+int64_t scan_step_workgroups(const ScanShape &s);
+
+struct NormShape {
+    int64_t rows, C, G, xp, zp;
+    float eps, scale;
+    bool gate_after, bf16, res_bf16;
+};
+hipError_t launch_norm(const NormShape &s, const void *x, const void *z, const void *residual,
+                       const float *weight, void *y, void *residual_out, hipStream_t st);
+int64_t norm_workgroups(const NormShape &s);
+
 // bf16 kernels (ssd_bf16.hip)
 hipError_t launch_state_pass_bf16(const Shape &s, const void *x, const void *B, const float *G2,
                                   const float *dtT, const float *h0, void *S, float *hT,
