@@ -331,7 +331,7 @@ typedef struct {
 
 /* Host-only checks: dimensions positive, split and pitch as described (a pitch is 0 or at
  * least the row's width) else SSD_ERR_BAD_SHAPE; dtype, width and flags in their sets,
- * seqlen <= 2^30, channels <= 2^24, batch * seqlen <= 2^31, pitch <= 2^28 and
+ * seqlen <= 2^30, channels <= 2^24, batch * seqlen <= 2^31, pitch <= 2^24 and
  * ceil(channels / 256) * ceil(seqlen / 8) * batch < 2^24 else SSD_ERR_UNSUPPORTED. */
 ssd_status ssd_conv_validate(const ssd_conv_problem *problem);
 
@@ -367,7 +367,7 @@ typedef struct {
 /* Host-only checks: dimensions positive, channels divisible by ngroups, a pitch 0 or at
  * least the row's width, else SSD_ERR_BAD_SHAPE; dstate a multiple of 8 up to 64, dtype and
  * flag in their sets, seqlen <= 2^30, channels <= 2^24, batch * seqlen <= 2^31, pitches <=
- * 2^28, batch * channels <= 2^31 / dstate and ngroups * ceil(channels / ngroups / 64) *
+ * 2^24, batch * channels <= 2^31 / dstate and ngroups * ceil(channels / ngroups / 64) *
  * batch < 2^20 else SSD_ERR_UNSUPPORTED. */
 ssd_status ssd_scan_validate(const ssd_scan_problem *problem);
 
@@ -412,7 +412,7 @@ typedef struct {
 
 /* Host-only checks: dimensions positive, channels divisible by ngroups, pitches as above
  * else SSD_ERR_BAD_SHAPE; dtypes, flag, eps and scale in their sets, channels <= 2^24,
- * pitches <= 2^28, rows <= 2^31 and rows * ngroups < 2^24 else SSD_ERR_UNSUPPORTED. */
+ * pitches <= 2^24, rows <= 2^31 and rows * ngroups < 2^24 else SSD_ERR_UNSUPPORTED. */
 ssd_status ssd_norm_validate(const ssd_norm_problem *problem);
 
 /* x, z, y [rows, channels]; z may be NULL (no gate); residual [rows, channels] may be NULL

@@ -11,7 +11,7 @@
 
 namespace {
 
-constexpr int64_t kMaxPitch = int64_t(1) << 28;
+constexpr int64_t kMaxPitch = int64_t(1) << 24;      // eight rows of fp32 within 2^29 bytes
 constexpr int64_t kMaxTokens = int64_t(1) << 30;
 constexpr int64_t kMaxRows = int64_t(1) << 31;       // batch * seqlen
 constexpr int64_t kMaxChannels = int64_t(1) << 24;

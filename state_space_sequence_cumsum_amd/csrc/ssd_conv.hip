@@ -124,6 +124,11 @@ template <typename T> ConvOut<T> out_of(const ConvShape &s, void *y0, void *y1, 
 int channel_tiles(const ConvShape &s) { return (int)((s.C + kConvThreads - 1) / kConvThreads); }
 int token_tiles(const ConvShape &s) { return (int)((s.L + kConvTokens - 1) / kConvTokens); }
 
+int64_t conv_workgroups(const ConvShape &s)
+{
+    return (int64_t)channel_tiles(s) * token_tiles(s) * s.b;
+}
+
 template <typename T, int K>
 hipError_t conv_go(const ConvShape &s, const void *x, const float *w, const float *bias,
                    const void *state0, const int32_t *lengths, void *y0, void *y1, void *y2,
@@ -147,11 +152,6 @@ hipError_t step_go(const ConvShape &s, const void *x, const float *w, const floa
 }
 
 }  // namespace
-
-int64_t conv_workgroups(const ConvShape &s)
-{
-    return (int64_t)channel_tiles(s) * token_tiles(s) * s.b;
-}
 
 hipError_t launch_conv(const ConvShape &s, const void *x, const float *w, const float *bias,
                        const void *state0, const int32_t *lengths, void *y0, void *y1, void *y2,

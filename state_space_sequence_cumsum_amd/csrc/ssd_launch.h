@@ -125,8 +125,6 @@ hipError_t launch_conv(const ConvShape &s, const void *x, const float *w, const 
 // One token per sequence (s.L = 1), state shifted in place.
 hipError_t launch_conv_step(const ConvShape &s, const void *x, const float *w, const float *bias,
                             void *state, void *y0, void *y1, void *y2, hipStream_t st);
-// Workgroups of either launch (256 threads each), for the grid check.
-int64_t conv_workgroups(const ConvShape &s);
 
 struct ScanShape {
     int64_t b, L, C, G, N;
@@ -147,12 +145,9 @@ struct ScanArgs {
     void *ws;
 };
 size_t scan_workspace_bytes(const ScanShape &s);
-// Workgroups of the largest launch, for the grid check.
-int64_t scan_workgroups(const ScanShape &s);
 hipError_t launch_scan(const ScanShape &s, const ScanArgs &a, hipStream_t st);
 // One token per sequence (s.L = 1), h [b, C, N] updated in place.
 hipError_t launch_scan_step(const ScanShape &s, const ScanArgs &a, float *h, hipStream_t st);
-int64_t scan_step_workgroups(const ScanShape &s);
 
 struct NormShape {
     int64_t rows, C, G, xp, zp;
@@ -161,7 +156,6 @@ struct NormShape {
 };
 hipError_t launch_norm(const NormShape &s, const void *x, const void *z, const void *residual,
                        const float *weight, void *y, void *residual_out, hipStream_t st);
-int64_t norm_workgroups(const NormShape &s);
 
 // bf16 kernels (ssd_bf16.hip)
 hipError_t launch_state_pass_bf16(const Shape &s, const void *x, const void *B, const float *G2,

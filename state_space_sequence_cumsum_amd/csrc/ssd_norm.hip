@@ -58,6 +58,8 @@ __global__ __launch_bounds__(kNormThreads) void norm_kernel(
     }
 }
 
+int64_t norm_workgroups(const NormShape &s) { return s.rows * s.G; }
+
 template <typename T, typename R>
 hipError_t norm_go(const NormShape &s, const void *x, const void *z, const void *residual,
                    const float *weight, void *y, void *residual_out, hipStream_t st)
@@ -70,8 +72,6 @@ hipError_t norm_go(const NormShape &s, const void *x, const void *z, const void 
 }
 
 }  // namespace
-
-int64_t norm_workgroups(const NormShape &s) { return s.rows * s.G; }
 
 hipError_t launch_norm(const NormShape &s, const void *x, const void *z, const void *residual,
                        const float *weight, void *y, void *residual_out, hipStream_t st)

@@ -5,10 +5,19 @@
 //     h_t[c, n] = exp(d_t[c] A[c, n]) h_{t-1}[c, n] + d_t[c] x_t[c] B_t[g, n]
 //     y_t[c]    = (sum_n C_t[g, n] h_t[c, n] + D[c] x_t[c]) silu(z_t[c])
 //
-// One lane owns a channel and keeps its N states and rates in registers; B_t and C_t are the
-// same for all lanes of a wave (one group per wave), so they come through scalar loads and
-// enter the products as scalar operands.  Per state and token: a product, an exp2 and three
-// more VALU operations, which bound the kernel before HBM does.
+// A wave owns 64 channels of one group, a lane one of them, with its N states and rates in
+// registers; B_t and C_t, the same for all lanes, are broadcast from LDS.  Per state and token:
+// two products, an exp2 (two VALU slots on gfx950) and two fused multiply-adds (one without the
+// output), which bound the scan before HBM does.  Where the channels give too few waves, the
+// tokens are split into segments: one launch scans each segment from zero for its end state, a
+// short one chains these into the segments' start states (exp of A times a segment's summed
+// steps is its decay), and one scans the segments again from there.  The first scan costs 0.8
+// of the second, and the bound is both.
+//
+// Measured (bf16, 16384 tokens, 2048 channels, 16 states, gate and softplus): 210 to 218 us (99
+// and 112 us for the scans, 4 to 5 us for the chain); the VALU slots of both scans are 198 us at
+// the 1.96 ns a slot and wave that an fma loop reaches, HBM's floor is 53 us.  One whole walk per channel: 5.3 ms.
+
 #include <hip/hip_runtime.h>
 
 #include "ssd_device.h"
@@ -23,20 +32,22 @@ __device__ __forceinline__ float silu(float v)
 }
 
 // log(1 + exp(v)) = max(v, 0) + log1p(e), e = exp(-|v|) in (0, 1], with
-// log1p(e) = 2 atanh(s), s = e / (2 + e) in (0, 1/3]; atanh(s) / s is a polynomial in s^2
-// (degree 4, interpolated at the Chebyshev points of [0, 1/9]: relative error 4.1e-9), so small
-// step sizes keep their relative accuracy (log2(1 + e) would not).
+// log1p(e) = 2 atanh(s), s = e / (2 + e): 2 s times a polynomial in (2 s)^2 (degree 4,
+// interpolated at the Chebyshev points of [0, 4/9]: relative error 4.1e-9), so small step sizes
+// keep their relative accuracy (log2(1 + e) would not).
 __device__ __forceinline__ float softplus(float v)
 {
     const float e = fast_exp2(-kLog2e * fabsf(v));
-    const float s = e * __builtin_amdgcn_rcpf(2.0f + e);
+    const float s = e * __builtin_amdgcn_rcpf(fmaf(0.5f, e, 1.0f));
     const float q = s * s;
-    float p = 0.14078889f;
-    p = fmaf(p, q, 0.13982579f);
-    p = fmaf(p, q, 0.20012298f);
-    p = fmaf(p, q, 0.33333161f);
+    float p = 5.4995661e-4f;
+    p = fmaf(p, q, 2.1847779e-3f);
+    p = fmaf(p, q, 1.2507686e-2f);
+    p = fmaf(p, q, 8.3332902e-2f);
     p = fmaf(p, q, 1.0f);
-    return fmaf(2.0f * s, p, fmaxf(v, 0.0f));
+    float top;   // fmaxf would spend an instruction on a signalling NaN
+    asm("v_max_f32 %0, 0, %1" : "=v"(top) : "v"(v));
+    return fmaf(s, p, top);
 }
 
 struct ScanDims {
@@ -44,52 +55,291 @@ struct ScanDims {
     int C, Cg, tiles;      // channels, channels per group, 64-channel tiles per group
     int G;
     int sp;                // 1: softplus
+    int S, seg;            // segments of the sequence, tokens per segment
 };
 
-template <typename T, int N>
-__global__ __launch_bounds__(64) void scan_kernel(
+// ---------------------------------------------------------------------------
+// The scan of one segment of tokens.  A wave owns 64 channels of one group; `KIND` says what
+// it computes:
+//   kWhole  the whole sequence: from h0, writes y and hT
+//   kEnds   one segment from a zero state: writes the state at its end and the sum of its steps
+//   kOut    one segment from the state at its start (workspace): writes y, the last one hT
+// ---------------------------------------------------------------------------
+enum Kind { kWhole, kEnds, kOut };
+
+// Four consecutive elements that start on a multiple of four bytes, as fp32.
+typedef uint32_t u32x2_a4 __attribute__((ext_vector_type(2), aligned(4)));
+typedef uint32_t u32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
+template <typename T> struct Quad;
+template <> struct Quad<float> {
+    u32x4 v;
+    __device__ __forceinline__ void load(const float *p) { v = *reinterpret_cast<const u32x4_a4 *>(p); }
+    __device__ __forceinline__ f32x4 get() const { return __builtin_bit_cast(f32x4, v); }
+};
+template <> struct Quad<bf16> {
+    u32x2 v;
+    __device__ __forceinline__ void load(const bf16 *p) { v = *reinterpret_cast<const u32x2_a4 *>(p); }
+    __device__ __forceinline__ f32x4 get() const
+    {
+        f32x4 f;
+        f[0] = bf_lo(v[0]); f[1] = bf_hi(v[0]); f[2] = bf_lo(v[1]); f[3] = bf_hi(v[1]);
+        return f;
+    }
+};
+
+// One element, as raw bits, at byte offset `off` (per lane) + `row` (uniform) of a raw buffer.
+template <typename T>
+__device__ __forceinline__ uint32_t buf_load(rsrc_t r, uint32_t off, uint32_t row)
+{
+    if constexpr (sizeof(T) == 2)
+        return (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, (int)off, (int)row, 0);
+    else
+        return (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(r, (int)off, (int)row, 0);
+}
+template <typename T> __device__ __forceinline__ float bits_to_f32(uint32_t v)
+{
+    return __uint_as_float(sizeof(T) == 2 ? v << 16 : v);
+}
+template <typename T>
+__device__ __forceinline__ void buf_store(rsrc_t r, uint32_t off, uint32_t row, T v)
+{
+    if constexpr (sizeof(T) == 2)
+        __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, v), r, (int)off, (int)row, 0);
+    else
+        __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), r, (int)off, (int)row, 0);
+}
+
+constexpr int kStep = 8;    // segments are multiples of this many tokens
+
+// The workspace of a split scan: per (sequence, segment), the state at the segment's end
+// (kEnds) and, after the combination, at its start, as [N][Cw] with Cw = G * tiles * 64, so
+// that a wave's lanes stand side by side; and the sum of its step sizes [Cw].
+struct ScanWs {
+    float *state, *steps;
+};
+
+template <typename T, int N, int KIND>
+__global__ __launch_bounds__(64) __attribute__((amdgpu_waves_per_eu(N <= 16 ? 4 : N <= 32 ? 3 : 2))) void scan_kernel(
     const T *__restrict__ x, const T *__restrict__ dt, const float *__restrict__ A,
     const T *__restrict__ B, const T *__restrict__ Cm, const float *__restrict__ D,
     const T *__restrict__ z, const float *__restrict__ dt_bias, const float *h0,
-    const int32_t *__restrict__ lengths, T *__restrict__ y, float *hT, ScanDims m)
+    const int32_t *__restrict__ lengths, T *__restrict__ y, float *hT, ScanWs ws, ScanDims m)
 {
-    const int tile = blockIdx.x % m.tiles;
-    const int g = blockIdx.x / m.tiles % m.G;
-    const int64_t b = blockIdx.x / m.tiles / m.G;
-    const int in_group = tile * 64 + threadIdx.x;
+    // tokens whose inputs a lane loads together, one tile ahead (as many as registers allow)
+    constexpr int kTile = N <= 16 ? 8 : 4;
+    // per token of the tile, B and (except for the end states) C as fp32; read by all lanes of
+    // the one wave, so each read is a broadcast
+    constexpr int kRow = KIND == kEnds ? N : 2 * N;
+    __shared__ __attribute__((aligned(16))) float bc[kTile * kRow];
+    const int gt = m.G * m.tiles;
+    const int wave = blockIdx.x % gt;
+    const int segs = KIND == kEnds ? m.S - 1 : m.S;
+    const int seg = blockIdx.x / gt % segs;
+    const int64_t b = blockIdx.x / gt / segs;
+    const int g = wave / m.tiles;
+    const int in_group = (wave % m.tiles) * 64 + threadIdx.x;
     const bool live = in_group < m.Cg;
     const int c = g * m.Cg + min(in_group, m.Cg - 1);
     int64_t len = m.L;
     if (lengths) len = min((int64_t)max(lengths[b], 0), m.L);
+    const int64_t t0 = (int64_t)seg * m.seg;
+    const int64_t t1 = KIND == kWhole ? len : min(t0 + m.seg, len);
+    const int count = (int)max(t1 - t0, (int64_t)0);
+    const int Cw = gt * 64;
+    const int64_t slot = b * m.S + seg;
+    const int cw = wave * 64 + threadIdx.x;
 
     float a2[N], h[N];
 #pragma unroll
-    for (int n = 0; n < N; ++n) a2[n] = kLog2e * A[(int64_t)c * N + n];
+    for (int n = 0; n < N; n += 4) {
+        const f32x4 v = *reinterpret_cast<const f32x4 *>(A + (int64_t)c * N + n);
 #pragma unroll
-    for (int n = 0; n < N; ++n) h[n] = h0 ? h0[(b * m.C + c) * N + n] : 0.0f;
-    const float bias = dt_bias ? dt_bias[c] : 0.0f;
-    const float Dv = D ? D[c] : 0.0f;
-    const T *xr = x + b * m.L * m.xp, *dr = dt + b * m.L * m.dtp;
-    const T *zr = z ? z + b * m.L * m.zp : nullptr;
-    const T *Br = B + b * m.L * m.Bp + g * N, *Cr = Cm + b * m.L * m.Cp + g * N;
-    T *yr = y + b * m.L * m.C;
-    for (int64_t t = 0; t < len; ++t) {
-        const float xv = (float)xr[t * m.xp + c];
-        float d = (float)dr[t * m.dtp + c] + bias;
-        if (m.sp) d = softplus(d);
-        const float u = d * xv;
-        float acc = Dv * xv;
-#pragma unroll
-        for (int n = 0; n < N; ++n) {
-            h[n] = fmaf(fast_exp2(d * a2[n]), h[n], u * (float)Br[t * m.Bp + n]);
-            acc = fmaf((float)Cr[t * m.Cp + n], h[n], acc);
-        }
-        if (zr) acc *= silu((float)zr[t * m.zp + c]);
-        if (live) yr[t * m.C + c] = Elem<T>::from_f32(acc);
+        for (int i = 0; i < 4; ++i) a2[n + i] = kLog2e * v[i];
     }
-    if (hT && live) {
 #pragma unroll
-        for (int n = 0; n < N; ++n) hT[(b * m.C + c) * N + n] = h[n];
+    for (int n = 0; n < N; ++n) h[n] = 0.0f;
+    if (KIND == kWhole && h0) {
+#pragma unroll
+        for (int n = 0; n < N; n += 4) {
+            const f32x4 v = *reinterpret_cast<const f32x4 *>(h0 + (b * m.C + c) * N + n);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) h[n + i] = v[i];
+        }
+    }
+    if (KIND == kOut) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) h[n] = ws.state[(slot * N + n) * Cw + cw];
+    }
+    const float bias = dt_bias ? dt_bias[c] : 0.0f;
+    const float Dv = KIND != kEnds && D ? D[c] : 0.0f;
+    float steps = 0.0f;
+
+    // A tile's rows are buffers that start at its first token's row; lane offset + row offset
+    // stay far below kRange (at most kTile rows of 2^24 elements).  Lanes past the group's end
+    // have an offset at its end: they read zeros and store nothing.
+    constexpr int kRange = 0x7ffffffe;
+    const int64_t row0 = b * m.L + t0;
+    const uint32_t lane_off = live ? (uint32_t)(c * sizeof(T)) : (uint32_t)kRange;
+    const bool gate = KIND != kEnds && z != nullptr;
+    const uint32_t xp = (uint32_t)m.xp * sizeof(T), dp = (uint32_t)m.dtp * sizeof(T),
+                   zp = gate ? (uint32_t)m.zp * sizeof(T) : 0;
+    const T *xr = x + row0 * m.xp, *dr = dt + row0 * m.dtp;
+    // without a gate the buffer is empty: its loads return zero and fetch nothing
+    const T *zr = gate ? z + row0 * m.zp : x;
+    const int z_range = gate ? kRange : 0;
+    T *yr = KIND != kEnds ? y + row0 * m.C : nullptr;
+
+    const T *Br = B + row0 * m.Bp + g * N, *Cr = Cm + row0 * m.Cp + g * N;
+
+    // One tile of all inputs ahead, in registers.  Rows past the last token read that token
+    // again and are not used.
+    constexpr int kQuads = kTile * kRow / 4;                 // of B and C in a tile
+    constexpr int kPer = (kQuads + 63) / 64;                 // per lane
+    uint32_t xn[kTile], dn[kTile], zn[kTile];
+    Quad<T> bn[kPer];
+    auto fetch = [&](int t) {
+        const rsrc_t xs = make_rsrc(xr + t * m.xp, kRange);
+        const rsrc_t ds = make_rsrc(dr + t * m.dtp, kRange);
+        const rsrc_t zs = make_rsrc(zr + (gate ? t * m.zp : 0), z_range);
+        const int last = count - 1 - t;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+            const int q = min((int)threadIdx.x + 64 * j, kQuads - 1);
+            const int64_t r = t + min(q / (kRow / 4), last);
+            const int n = q % (kRow / 4) * 4;
+            bn[j].load(KIND == kEnds || n < N ? Br + r * m.Bp + n : Cr + r * m.Cp + (n - N));
+        }
+#pragma unroll
+        for (int i = 0; i < kTile; ++i) {
+            const int r = min(i, last);
+            xn[i] = buf_load<T>(xs, lane_off, r * xp);
+            dn[i] = buf_load<T>(ds, lane_off, r * dp);
+            if (KIND != kEnds) zn[i] = buf_load<T>(zs, lane_off, r * zp);
+        }
+    };
+    if (count > 0) fetch(0);
+    for (int t = 0; t < count; t += kTile) {
+        // One wave: its LDS accesses are carried out in order, so the tile is written over the
+        // previous one's reads without a barrier.
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+            const int q = (int)threadIdx.x + 64 * j;
+            if (kQuads % 64 == 0 || q < kQuads) *reinterpret_cast<f32x4 *>(bc + 4 * q) = bn[j].get();
+        }
+        float xv[kTile], dv[kTile], zv[kTile];
+#pragma unroll
+        for (int i = 0; i < kTile; ++i) {
+            xv[i] = bits_to_f32<T>(xn[i]);
+            dv[i] = bits_to_f32<T>(dn[i]) + bias;
+            zv[i] = KIND != kEnds ? bits_to_f32<T>(zn[i]) : 0.0f;
+        }
+        if (m.sp) {
+#pragma unroll
+            for (int i = 0; i < kTile; ++i) dv[i] = softplus(dv[i]);
+        }
+        if (t + kTile < count) fetch(t + kTile);
+#pragma unroll
+        for (int i = 0; i < kTile; ++i) {
+            if (t + i >= count) break;
+            const float u = dv[i] * xv[i];
+            if (KIND == kEnds) steps += dv[i];
+            float acc = Dv * xv[i];
+#pragma unroll
+            for (int n = 0; n < N; n += 4) {
+                const f32x4 bv = *reinterpret_cast<const f32x4 *>(bc + i * kRow + n);
+                f32x4 cv;
+                if (KIND != kEnds) cv = *reinterpret_cast<const f32x4 *>(bc + i * kRow + N + n);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float a = fast_exp2(dv[i] * a2[n + k]);
+                    // (the product that replaces h and the sum in its place: no register moves)
+                    h[n + k] = fmaf(u, bv[k], a * h[n + k]);
+                    if (KIND != kEnds) acc = fmaf(cv[k], h[n + k], acc);
+                }
+            }
+            if (KIND != kEnds) {
+                if (gate) acc *= silu(zv[i]);
+                buf_store<T>(make_rsrc(yr, kRange), lane_off, 0, Elem<T>::from_f32(acc));
+                yr += m.C;
+            }
+        }
+    }
+    if (KIND == kEnds) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) ws.state[(slot * N + n) * Cw + cw] = h[n];
+        ws.steps[slot * Cw + cw] = steps;
+    } else if (hT && live && seg == m.S - 1) {
+#pragma unroll
+        for (int n = 0; n < N; n += 4) {
+            f32x4 v;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = h[n + i];
+            *reinterpret_cast<f32x4 *>(hT + (b * m.C + c) * N + n) = v;
+        }
+    }
+}
+
+// Turns the segments' end states (each from zero) into their start states, in place: along
+// the segments, start[0] = h0 and start[s + 1] = exp(A sum of steps of s) start[s] + end[s].
+// A workgroup owns 64 channels and one state; its waves take runs of segments, load them all at
+// once, form each run's own decay and end, and after an exchange through LDS walk their runs
+// from the true start: two trips to memory whatever the number of segments in a round.
+constexpr int kRunWaves = 8, kRun = 16;     // at most: waves of a workgroup, segments of a run
+__global__ __launch_bounds__(64 * kRunWaves) void scan_combine_kernel(const float *__restrict__ A,
+                                                                      const float *h0, ScanWs ws,
+                                                                      int N, ScanDims m)
+{
+    __shared__ float run_decay[kRunWaves][64], run_end[kRunWaves][64];
+    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+    const int gt = m.G * m.tiles;
+    const int wave = blockIdx.x % gt, n = blockIdx.x / gt % N;
+    const int64_t b = blockIdx.x / gt / N;
+    const int64_t Cw = (int64_t)gt * 64;
+    const int in_group = (wave % m.tiles) * 64 + lane;
+    const bool live = in_group < m.Cg;
+    const int c = wave / m.tiles * m.Cg + min(in_group, m.Cg - 1);
+    const float a2 = kLog2e * A[(int64_t)c * N + n];
+    float h = h0 && live ? h0[(b * m.C + c) * N + n] : 0.0f;
+    float *st = ws.state + (b * m.S * N + n) * Cw + wave * 64 + lane;
+    const float *sm = ws.steps + b * m.S * Cw + wave * 64 + lane;
+    // segments 0 .. S - 2 have an end state; start states are written for 0 .. S - 1
+    const int nw = blockDim.x >> 6;
+    for (int s0 = 0; s0 < m.S; s0 += nw * kRun) {
+        const int per = min((m.S - s0 + nw - 1) / nw, kRun);
+        const int first = s0 + wv * per;
+        float e[kRun], d[kRun];
+#pragma unroll
+        for (int i = 0; i < kRun; ++i) {
+            if (i < per) {
+                const int64_t s = min(first + i, m.S - 2);
+                e[i] = st[s * N * Cw];
+                d[i] = sm[s * Cw];
+            }
+        }
+        float decay = 1.0f, end = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kRun; ++i) {
+            const bool on = i < per && first + i < m.S - 1;
+            d[i] = on ? fast_exp2(a2 * d[i]) : 1.0f;
+            e[i] = on ? e[i] : 0.0f;
+            end = fmaf(d[i], end, e[i]);
+            decay *= d[i];
+        }
+        run_decay[wv][lane] = decay;
+        run_end[wv][lane] = end;
+        __syncthreads();
+        float mine = h;
+#pragma unroll
+        for (int w = 0; w < kRunWaves; ++w) {
+            if (w == wv) mine = h;
+            if (w < nw) h = fmaf(run_decay[w][lane], h, run_end[w][lane]);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kRun; ++i) {
+            if (i < per && first + i < m.S) st[(int64_t)(first + i) * N * Cw] = mine;
+            mine = fmaf(d[i], mine, e[i]);
+        }
     }
 }
 
@@ -124,6 +374,30 @@ __global__ __launch_bounds__(64) void scan_step_kernel(
     y[b * m.C + c] = Elem<T>::from_f32(acc);
 }
 
+// Segments that a sequence is split into, and tokens in each (a multiple of kStep); `waves`
+// waves of 64 channels would walk whole sequences.
+//   - From 1024 of them (one a SIMD) the sequences stay whole: the end states cost most of a
+//     second walk, which more waves then no longer make up for (16 x 4096 tokens, 4096 channels
+//     of 16 states: 1370 us whole, 1428 us in four segments; half as many sequences and channels,
+//     2048 tokens: 709 whole, 404 in eight).
+//   - So do sequences under 32 tokens, where two more launches cost more than a walk (16 tokens:
+//     7.8 us whole, 12.0 split; 32 tokens: 13.0 and 12.1).
+//   - Else up to about 4096 waves (one 16384-token sequence of 2048 channels: 231 us with 2048
+//     waves, 210 with 4096, 210 with 6144), in segments of 16 tokens at least, or of 8 where
+//     even these are few (256 tokens, 256 channels: 12.6 us against 16.6).
+void split_of(const ScanShape &s, int64_t waves, int &S, int &seg)
+{
+    int64_t tokens = s.L;
+    if (waves < 1024 && s.L >= 32) {
+        const int64_t least = waves * s.L <= 8 * 2048 ? 8 : 16;
+        tokens = (waves * s.L + 4095) / 4096;
+        if (tokens < least) tokens = least;
+    }
+    tokens = (tokens + kStep - 1) / kStep * kStep;
+    seg = (int)tokens;
+    S = (int)((s.L + tokens - 1) / tokens);
+}
+
 ScanDims dims_of(const ScanShape &s)
 {
     ScanDims m;
@@ -131,23 +405,49 @@ ScanDims dims_of(const ScanShape &s)
     m.C = (int)s.C; m.G = (int)s.G; m.Cg = (int)(s.C / s.G);
     m.tiles = (m.Cg + 63) / 64;
     m.sp = s.softplus;
+    split_of(s, (int64_t)m.tiles * m.G * s.b, m.S, m.seg);
     return m;
+}
+
+int64_t waves_of(const ScanShape &s, const ScanDims &m) { return (int64_t)m.tiles * m.G * s.b; }
+
+int64_t scan_step_workgroups(const ScanShape &s) { return waves_of(s, dims_of(s)); }
+
+template <typename T, int N, int KIND>
+hipError_t scan_pass(const ScanShape &s, const ScanDims &m, const ScanWs &ws, const ScanArgs &a,
+                     hipStream_t st)
+{
+    const int64_t waves = waves_of(s, m) * (KIND == kEnds ? m.S - 1 : m.S);
+    hipLaunchKernelGGL((scan_kernel<T, N, KIND>), dim3((unsigned)waves), dim3(64), 0, st,
+                       (const T *)a.x, (const T *)a.dt, a.A, (const T *)a.B, (const T *)a.C, a.D,
+                       (const T *)a.z, a.dt_bias, a.h0, a.lengths, (T *)a.y, a.hT, ws, m);
+    return hipGetLastError();
 }
 
 template <typename T, int N>
 hipError_t scan_go(const ScanShape &s, const ScanArgs &a, float *h, hipStream_t st)
 {
     const ScanDims m = dims_of(s);
-    const dim3 grid((unsigned)scan_workgroups(s));
-    if (h)
-        hipLaunchKernelGGL((scan_step_kernel<T, N>), grid, dim3(64), 0, st, (const T *)a.x,
-                           (const T *)a.dt, a.A, (const T *)a.B, (const T *)a.C, a.D,
-                           (const T *)a.z, a.dt_bias, h, (T *)a.y, m);
-    else
-        hipLaunchKernelGGL((scan_kernel<T, N>), grid, dim3(64), 0, st, (const T *)a.x,
-                           (const T *)a.dt, a.A, (const T *)a.B, (const T *)a.C, a.D,
-                           (const T *)a.z, a.dt_bias, a.h0, a.lengths, (T *)a.y, a.hT, m);
-    return hipGetLastError();
+    if (h) {
+        hipLaunchKernelGGL((scan_step_kernel<T, N>), dim3((unsigned)scan_step_workgroups(s)),
+                           dim3(64), 0, st, (const T *)a.x, (const T *)a.dt, a.A, (const T *)a.B,
+                           (const T *)a.C, a.D, (const T *)a.z, a.dt_bias, h, (T *)a.y, m);
+        return hipGetLastError();
+    }
+    const int64_t Cw = (int64_t)m.G * m.tiles * 64;
+    ScanWs ws;
+    ws.state = (float *)a.ws;
+    ws.steps = ws.state + s.b * m.S * N * Cw;
+    if (m.S == 1) return scan_pass<T, N, kWhole>(s, m, ws, a, st);
+    hipError_t e = scan_pass<T, N, kEnds>(s, m, ws, a, st);
+    if (e != hipSuccess) return e;
+    // runs of eight segments or more
+    const int run_waves = m.S >= 8 * kRunWaves ? kRunWaves : (m.S + 7) / 8;
+    hipLaunchKernelGGL(scan_combine_kernel, dim3((unsigned)(m.G * m.tiles * N * s.b)),
+                       dim3(64 * run_waves), 0, st, a.A, a.h0, ws, N, m);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    return scan_pass<T, N, kOut>(s, m, ws, a, st);
 }
 
 template <typename T>
@@ -168,14 +468,12 @@ hipError_t scan_by_state(const ScanShape &s, const ScanArgs &a, float *h, hipStr
 
 }  // namespace
 
-size_t scan_workspace_bytes(const ScanShape &) { return 256; }
-
-int64_t scan_workgroups(const ScanShape &s)
+size_t scan_workspace_bytes(const ScanShape &s)
 {
     const ScanDims m = dims_of(s);
-    return (int64_t)m.tiles * m.G * s.b;
+    if (m.S == 1) return 256;
+    return (size_t)s.b * m.S * (s.N + 1) * m.G * m.tiles * 64 * sizeof(float);
 }
-int64_t scan_step_workgroups(const ScanShape &s) { return scan_workgroups(s); }
 
 hipError_t launch_scan(const ScanShape &s, const ScanArgs &a, hipStream_t st)
 {
