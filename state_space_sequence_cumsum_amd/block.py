@@ -13,7 +13,7 @@ import ctypes
 import torch
 
 from . import binding
-from .binding import SSD_BF16, SSD_F32, _raise, _stream
+from .binding import SSD_BF16, SSD_F32, _raise
 
 _DTYPES = {torch.float32: SSD_F32, torch.bfloat16: SSD_BF16}
 
@@ -61,13 +61,14 @@ def lib():
 
 
 # ---------------------------------------------------------------------------
-# tensor checks
+# tensor checks: one test of everything first, the reason for a refusal only where it fails
+# (these run for every tensor of every call)
 # ---------------------------------------------------------------------------
-def _check(t, name, dtype, shape, device):
+def _refuse(t, name, dtype, shape, device):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if device is not None and t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{device}")
     if t.dtype != dtype:
         raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if t.shape != shape:
@@ -75,20 +76,20 @@ def _check(t, name, dtype, shape, device):
 
 
 def _dense(t, name, dtype, shape, device):
-    """The address of a contiguous tensor (None for None)."""
+    """The address of a contiguous tensor on GPU `device` (None for None)."""
     if t is None:
         return None
-    _check(t, name, dtype, shape, device)
-    if not t.is_contiguous():
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.get_device() == device and t.is_contiguous()):
+        _refuse(t, name, dtype, shape, device)
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
 
 
-def _rows(t, name, dtype, shape, device, lead):
-    """(address, pitch) of a tensor whose first `lead` dimensions count tokens: the others
-    are dense, and the tokens follow each other at one pitch."""
-    _check(t, name, dtype, shape, device)
-    stride, width = t.stride(), 1
+def _pitch(t, name, lead):
+    """Elements between the tokens of a tensor whose first `lead` dimensions count tokens: the
+    others are dense, and the tokens follow each other at one pitch (0: dense tokens)."""
+    shape, stride, width = t.shape, t.stride(), 1
     for d in range(len(shape) - 1, lead - 1, -1):
         if shape[d] != 1 and stride[d] != width:
             raise ValueError(f"{name} must have dense rows")
@@ -103,83 +104,106 @@ def _rows(t, name, dtype, shape, device, lead):
             if stride[d] != pitch * tokens:
                 raise ValueError(f"{name} must have one pitch from token to token")
         tokens *= shape[d]
-    return t.data_ptr(), pitch
+    return pitch
+
+
+def _rows(t, name, dtype, shape, device, lead):
+    """(address, pitch) of a tensor on GPU `device` that _pitch takes."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.get_device() == device):
+        _refuse(t, name, dtype, shape, device)
+    return t.data_ptr(), 0 if t.is_contiguous() else _pitch(t, name, lead)
 
 
 def _io(x, name="x"):
-    code = _DTYPES.get(x.dtype) if isinstance(x, torch.Tensor) else None
+    """(dtype code, GPU index) of the tensor that sets both."""
+    code = _DTYPES.get(x.dtype) if isinstance(x, torch.Tensor) and x.is_cuda else None
     if code is None:
         raise ValueError(f"{name} must be a float32 or bfloat16 GPU tensor")
-    return code
+    return code, x.get_device()
 
 
-class _Call:
-    """A C entry point with checked arguments: what a plan keeps and a function calls once."""
+def _empty(shape, dtype, device):
+    return torch.empty(shape, dtype=dtype, device=device)
 
-    __slots__ = ("fn", "args", "device", "what", "keep")
 
-    def __init__(self, fn, args, device, what, keep):
-        self.fn, self.args, self.device, self.what, self.keep = fn, args, device, what, keep
+def _stream(stream, device):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
-    def __call__(self):
-        # kernels are launched for the tensors' device, whichever is current
-        if torch.cuda.current_device() == self.device.index:
-            st = self.fn(*self.args)
-        else:
-            with torch.cuda.device(self.device):
-                st = self.fn(*self.args)
-        if st != 0:
-            _raise(st, self.what)
+
+def _call(fn, args, device, what):
+    """Calls a C entry point: kernels are launched for the tensors' GPU, whichever is current."""
+    if torch.cuda.current_device() == device:
+        st = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args)
+    if st != 0:
+        _raise(st, what)
+
+
+class _Bound:
+    """A C entry point bound to fixed tensors (kept alive here); run() only calls it."""
+
+    def __init__(self, fn, args, device, what, keep, y):
+        self._fn, self._args, self._device, self._what = fn, args, device, what
+        self._keep, self.y = keep, y
+
+    def run(self):
+        """One step; returns y (the same tensors every call)."""
+        _call(self._fn, self._args, self._device, self._what)
+        return self.y
 
 
 # ---------------------------------------------------------------------------
 # short causal convolution
 # ---------------------------------------------------------------------------
-def _conv_call(x, weight, bias, state, silu, lengths, split, y, final_state, want_final, stream,
+def _conv_args(x, weight, bias, state, silu, lengths, split, y, final_state, want_final, stream,
                step):
+    """(arguments of the entry point, GPU, outputs, final state, tensors to keep)."""
     what = "ssd_conv_step" if step else "ssd_conv"
-    code = _io(x)
-    if x.dim() != (2 if step else 3):
+    code, dev = _io(x)
+    shape, td = x.shape, x.dtype
+    if len(shape) != (2 if step else 3):
         raise ValueError(f"{what} takes x " + ("[b, channels]" if step else "[b, L, channels]"))
-    if weight.dim() != 2:
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
         raise ValueError("weight must be [channels, width]")
-    td, dev, lead = x.dtype, x.device, tuple(x.shape[:-1])
-    b, c = x.shape[0], x.shape[-1]
-    k = weight.shape[1]
-    one = split is None
-    widths = [c] if one else [int(w) for w in split]
-    if not 1 <= len(widths) <= 3 or sum(widths) != c or min(widths) <= 0:
-        raise ValueError(f"split {widths} must be 1 to 3 positive widths with sum {c}")
-    xp, pitch = _rows(x, "x", td, x.shape, None, len(lead))
+    b, c, k = shape[0], shape[-1], weight.shape[1]
+    lead = tuple(shape[:-1])
+    widths = (c,) if split is None else tuple(split)
+    n = len(widths)
+    if not 1 <= n <= 3 or sum(widths) != c or min(widths) <= 0:
+        raise ValueError(f"split {list(widths)} must be 1 to 3 positive widths with sum {c}")
+    xp, pitch = _rows(x, "x", td, shape, dev, len(lead))
     wp = _dense(weight, "weight", torch.float32, (c, k), dev)
     bp = _dense(bias, "bias", torch.float32, (c,), dev)
     sp = _dense(state, "state", td, (b, k - 1, c), dev)
     if y is None:
-        ys = [torch.empty(*lead, w, device=dev, dtype=td) for w in widths]
+        ys = tuple([_empty((*lead, w), td, x.device) for w in widths])
+        yp = [t.data_ptr() for t in ys]
     else:
-        ys = [y] if isinstance(y, torch.Tensor) else list(y)
-    if len(ys) != len(widths):
-        raise ValueError(f"y must be {len(widths)} tensors, one per split width")
-    yp = [_dense(t, "y", td, (*lead, w), dev) for t, w in zip(ys, widths)]
-    yp += [None] * (3 - len(yp))
-    prob = ConvProblem(b, 1 if step else x.shape[1], c, pitch,
-                       (ctypes.c_int64 * 3)(*widths, *[0] * (3 - len(widths))), k, int(bool(silu)),
-                       code)
-    out = ys[0] if one else tuple(ys)
+        ys = (y,) if isinstance(y, torch.Tensor) else tuple(y)
+        if len(ys) != n:
+            raise ValueError(f"y must be {n} tensors, one per split width")
+        yp = [_dense(t, "y", td, (*lead, w), dev) for t, w in zip(ys, widths)]
+        if None in yp:
+            raise ValueError("y must be a GPU tensor")
+    yp += [None] * (3 - n)
+    prob = ConvProblem(b, 1 if step else shape[1], c, pitch, widths, k, 1 if silu else 0, code)
+    out = ys[0] if split is None else ys
     if step:
         if state is None:
             raise ValueError("state must be a GPU tensor")
         args = (ctypes.byref(prob), xp, wp, bp, sp, *yp, _stream(stream, dev))
-        call = _Call(lib().ssd_conv_step, args, dev, what, (prob, x, weight, bias, state, ys))
-        return call, out, state
+        return args, dev, out, state, (x, weight, bias, state, ys)
     lp = _dense(lengths, "lengths", torch.int32, (b,), dev)
     if final_state is None and want_final:
-        final_state = torch.empty(b, k - 1, c, device=dev, dtype=td)
+        final_state = _empty((b, k - 1, c), td, x.device)
     fp = _dense(final_state, "final_state", td, (b, k - 1, c), dev)
     args = (ctypes.byref(prob), xp, wp, bp, sp, lp, *yp, fp, _stream(stream, dev))
-    call = _Call(lib().ssd_conv, args, dev, what, (prob, x, weight, bias, state, lengths, ys,
-                                                   final_state))
-    return call, out, final_state
+    return args, dev, out, final_state, None
 
 
 def ssd_conv(x, weight, bias=None, state=None, *, silu=True, lengths=None, split=None, y=None,
@@ -193,63 +217,63 @@ def ssd_conv(x, weight, bias=None, state=None, *, silu=True, lengths=None, split
     ``lengths`` [b] int32: tokens of each sequence; rows of y behind them are left as they
     were.  ``final_state`` may be ``state`` itself.  Returns (y or a tuple of them, final
     state or None)."""
-    call, out, final = _conv_call(x, weight, bias, state, silu, lengths, split, y, final_state,
-                                  want_final, stream, False)
-    call()
+    args, dev, out, final, _ = _conv_args(x, weight, bias, state, silu, lengths, split, y,
+                                          final_state, want_final, stream, False)
+    _call(lib().ssd_conv, args, dev, "ssd_conv")
     return out, final
 
 
 def ssd_conv_step(x, weight, bias, state, *, silu=True, split=None, y=None, stream=None):
     """The convolution for one token per sequence: x [b, channels]; state [b, width-1,
     channels] is shifted in place.  Returns y, or a tuple of them where ``split`` is given."""
-    call, out, _ = _conv_call(x, weight, bias, state, silu, None, split, y, None, False, stream,
-                              True)
-    call()
+    args, dev, out, _, _ = _conv_args(x, weight, bias, state, silu, None, split, y, None, False,
+                                      stream, True)
+    _call(lib().ssd_conv_step, args, dev, "ssd_conv_step")
     return out
 
 
-class ConvStepPlan:
+class ConvStepPlan(_Bound):
     """ssd_conv_step bound to fixed tensors, for decode loops: the arguments are checked
     once, and run() only calls the C entry point (the caller refills x in place; state is
     updated in place).  The stream is fixed when the plan is made."""
 
     def __init__(self, x, weight, bias, state, *, silu=True, split=None, y=None, stream=None):
-        self._call, self.y, _ = _conv_call(x, weight, bias, state, silu, None, split, y, None,
-                                           False, stream, True)
-
-    def run(self):
-        """One step; returns y (the same tensors every call)."""
-        self._call()
-        return self.y
+        args, dev, out, _, keep = _conv_args(x, weight, bias, state, silu, None, split, y, None,
+                                             False, stream, True)
+        super().__init__(lib().ssd_conv_step, args, dev, "ssd_conv_step", keep, out)
 
 
 # ---------------------------------------------------------------------------
 # selective scan
 # ---------------------------------------------------------------------------
-def _scan_problem(x, dt, A, B, C, z, dt_softplus, lead):
-    code = _io(x)
-    if x.dim() != lead + 1 or B.dim() != lead + 2 or A.dim() != 2:
+def _scan_inputs(x, dt, A, B, C, D, z, dt_bias, dt_softplus, lead):
+    """(problem, GPU, addresses of x, dt, A, B, C, D, z, dt_bias)."""
+    code, dev = _io(x)
+    shape, td, f32 = x.shape, x.dtype, torch.float32
+    if not (isinstance(A, torch.Tensor) and isinstance(B, torch.Tensor) and len(shape) == lead + 1
+            and B.dim() == lead + 2 and A.dim() == 2):
         names = "[b, L, channels]" if lead == 2 else "[b, channels]"
         raise ValueError(f"the scan takes x {names}, B with [ngroups, dstate] in place of "
                          "channels, and A [channels, dstate]")
-    td, dev = x.dtype, x.device
-    c, (G, N) = x.shape[-1], B.shape[-2:]
-    xp, x_pitch = _rows(x, "x", td, x.shape, None, lead)
-    dp, dt_pitch = _rows(dt, "dt", td, x.shape, dev, lead)
-    ap = _dense(A, "A", torch.float32, (c, N), dev)
-    bc = (*x.shape[:-1], G, N)
+    b, L, c = shape[0], shape[1] if lead == 2 else 1, shape[-1]
+    G, N = B.shape[-2:]
+    bc = (b, L, G, N) if lead == 2 else (b, G, N)
+    xp, x_pitch = _rows(x, "x", td, shape, dev, lead)
+    dp, dt_pitch = _rows(dt, "dt", td, shape, dev, lead)
+    ap = _dense(A, "A", f32, (c, N), dev)
     bp, b_pitch = _rows(B, "B", td, bc, dev, lead)
     cp, c_pitch = _rows(C, "C", td, bc, dev, lead)
-    zp, z_pitch = (None, 0) if z is None else _rows(z, "z", td, x.shape, dev, lead)
-    prob = ScanProblem(x.shape[0], x.shape[1] if lead == 2 else 1, c, G, N, x_pitch, dt_pitch,
-                       z_pitch, b_pitch, c_pitch, int(bool(dt_softplus)), code)
-    return prob, td, dev, (xp, dp, ap, bp, cp), zp
+    Dp = _dense(D, "D", f32, (c,), dev)
+    zp, z_pitch = (None, 0) if z is None else _rows(z, "z", td, shape, dev, lead)
+    tp = _dense(dt_bias, "dt_bias", f32, (c,), dev)
+    prob = ScanProblem(b, L, c, G, N, x_pitch, dt_pitch, z_pitch, b_pitch, c_pitch,
+                       1 if dt_softplus else 0, code)
+    return prob, dev, (xp, dp, ap, bp, cp, Dp, zp, tp)
 
 
 def scan_problem(x, B, *, dt_softplus=False) -> ScanProblem:
     """The problem of a scan over dense x [b, L, channels] and B [b, L, ngroups, dstate]."""
-    return ScanProblem(x.shape[0], x.shape[1], x.shape[2], B.shape[2], B.shape[3], 0, 0, 0, 0, 0,
-                       int(bool(dt_softplus)), _io(x))
+    return ScanProblem(*x.shape, *B.shape[2:], 0, 0, 0, 0, 0, int(bool(dt_softplus)), _io(x)[0])
 
 
 def ssd_scan_workspace_bytes(problem: ScanProblem) -> int:
@@ -267,69 +291,61 @@ def ssd_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, *, dt_softpl
     ``lengths`` [b] int32: tokens of each sequence; rows of y behind them are left as they
     were and hT is the state after each sequence's own last token.  hT may be h0 itself.
     Returns (y [b, L, channels], hT [b, channels, dstate] float32 or None)."""
-    prob, td, dev, ptrs, zp = _scan_problem(x, dt, A, B, C, z, dt_softplus, 2)
-    b, c, N = prob.batch, prob.channels, prob.dstate
-    vec = [_dense(t, n, torch.float32, (c,), dev) for t, n in ((D, "D"), (dt_bias, "dt_bias"))]
-    hp = _dense(h0, "h0", torch.float32, (b, c, N), dev)
-    lp = _dense(lengths, "lengths", torch.int32, (b,), dev)
+    prob, dev, ptrs = _scan_inputs(x, dt, A, B, C, D, z, dt_bias, dt_softplus, 2)
+    td, f32 = x.dtype, torch.float32
+    states = (prob.batch, prob.channels, prob.dstate)
+    hp = _dense(h0, "h0", f32, states, dev)
+    lp = _dense(lengths, "lengths", torch.int32, (prob.batch,), dev)
     if y is None:
-        y = torch.empty(x.shape, device=dev, dtype=td)
+        y = _empty(x.shape, td, x.device)
     yp = _dense(y, "y", td, x.shape, dev)
     if hT is None and want_final:
-        hT = torch.empty(b, c, N, device=dev, dtype=torch.float32)
-    tp = _dense(hT, "hT", torch.float32, (b, c, N), dev)
-    L = lib()
+        hT = _empty(states, f32, x.device)
+    tp = _dense(hT, "hT", f32, states, dev)
+    L, p = lib(), ctypes.byref(prob)
     if workspace is None:
-        n = L.ssd_scan_workspace_bytes(ctypes.byref(prob))
+        n = L.ssd_scan_workspace_bytes(p)
         if n == 0:
-            _raise(L.ssd_scan_validate(ctypes.byref(prob)), "ssd_scan")
-        workspace = torch.empty(n, device=dev, dtype=torch.uint8)
-    elif not workspace.is_cuda or workspace.device != dev or not workspace.is_contiguous():
+            _raise(L.ssd_scan_validate(p), "ssd_scan")
+        workspace = _empty(n, torch.uint8, x.device)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the inputs' device")
-    _Call(L.ssd_scan, (ctypes.byref(prob), *ptrs, vec[0], zp, vec[1], hp, lp, yp, tp,
-                       workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                       _stream(stream, dev)), dev, "ssd_scan", None)()
+    _call(L.ssd_scan, (p, *ptrs, hp, lp, yp, tp, workspace.data_ptr(),
+                       workspace.numel() * workspace.element_size(), _stream(stream, dev)), dev,
+          "ssd_scan")
     return y, hT
 
 
-def _scan_step_call(x, dt, A, B, C, h, D, z, dt_bias, dt_softplus, y, stream):
-    prob, td, dev, ptrs, zp = _scan_problem(x, dt, A, B, C, z, dt_softplus, 1)
-    c, N = prob.channels, prob.dstate
-    vec = [_dense(t, n, torch.float32, (c,), dev) for t, n in ((D, "D"), (dt_bias, "dt_bias"))]
+def _scan_step_args(x, dt, A, B, C, h, D, z, dt_bias, dt_softplus, y, stream):
+    prob, dev, ptrs = _scan_inputs(x, dt, A, B, C, D, z, dt_bias, dt_softplus, 1)
     if h is None:
         raise ValueError("h must be a GPU tensor")
-    hp = _dense(h, "h", torch.float32, (prob.batch, c, N), dev)
+    hp = _dense(h, "h", torch.float32, (prob.batch, prob.channels, prob.dstate), dev)
     if y is None:
-        y = torch.empty(x.shape, device=dev, dtype=td)
-    yp = _dense(y, "y", td, x.shape, dev)
-    args = (ctypes.byref(prob), *ptrs, vec[0], zp, vec[1], hp, yp, _stream(stream, dev))
-    return _Call(lib().ssd_scan_step, args, dev, "ssd_scan_step",
-                 (prob, x, dt, A, B, C, h, D, z, dt_bias, y)), y
+        y = _empty(x.shape, x.dtype, x.device)
+    yp = _dense(y, "y", x.dtype, x.shape, dev)
+    return (ctypes.byref(prob), *ptrs, hp, yp, _stream(stream, dev)), dev, y
 
 
 def ssd_scan_step(x, dt, A, B, C, h, D=None, z=None, dt_bias=None, *, dt_softplus=False, y=None,
                   stream=None):
     """The scan for one token per sequence: x, dt, z [b, channels], B and C [b, ngroups,
     dstate]; h [b, channels, dstate] float32 is updated in place.  Returns y [b, channels]."""
-    call, y = _scan_step_call(x, dt, A, B, C, h, D, z, dt_bias, dt_softplus, y, stream)
-    call()
+    args, dev, y = _scan_step_args(x, dt, A, B, C, h, D, z, dt_bias, dt_softplus, y, stream)
+    _call(lib().ssd_scan_step, args, dev, "ssd_scan_step")
     return y
 
 
-class ScanStepPlan:
+class ScanStepPlan(_Bound):
     """ssd_scan_step bound to fixed tensors, for decode loops: the arguments are checked
     once, and run() only calls the C entry point (the caller refills x, dt, B, C and z in
     place; h is updated in place).  The stream is fixed when the plan is made."""
 
     def __init__(self, x, dt, A, B, C, h, D=None, z=None, dt_bias=None, *, dt_softplus=False,
                  y=None, stream=None):
-        self._call, self.y = _scan_step_call(x, dt, A, B, C, h, D, z, dt_bias, dt_softplus, y,
-                                             stream)
-
-    def run(self):
-        """One step; returns y (the same tensor every call)."""
-        self._call()
-        return self.y
+        args, dev, y = _scan_step_args(x, dt, A, B, C, h, D, z, dt_bias, dt_softplus, y, stream)
+        super().__init__(lib().ssd_scan_step, args, dev, "ssd_scan_step",
+                         (x, dt, A, B, C, h, D, z, dt_bias), y)
 
 
 # ---------------------------------------------------------------------------
@@ -345,32 +361,32 @@ def ssd_norm(x, weight, z=None, residual=None, *, ngroups=1, eps=1e-5, scale=1.0
     or x's dtype) the norm takes residual + scale * x (the gate applied), which is also
     stored to ``residual_out`` (may be ``residual`` itself).  Returns y, or (y,
     residual_out) with a residual (None in its place unless ``want_residual``)."""
-    code = _io(x)
-    if x.dim() < 1:
+    code, dev = _io(x)
+    shape, td = x.shape, x.dtype
+    if len(shape) < 1:
         raise ValueError("ssd_norm takes x [..., channels]")
-    td, dev, c = x.dtype, x.device, x.shape[-1]
-    lead = x.dim() - 1
-    xp, x_pitch = _rows(x, "x", td, x.shape, None, lead)
-    zp, z_pitch = (None, 0) if z is None else _rows(z, "z", td, x.shape, dev, lead)
+    c, lead = shape[-1], len(shape) - 1
+    xp, x_pitch = _rows(x, "x", td, shape, dev, lead)
+    zp, z_pitch = (None, 0) if z is None else _rows(z, "z", td, shape, dev, lead)
     wp = _dense(weight, "weight", torch.float32, (c,), dev)
     rp = op = None
     rcode = SSD_F32
     if residual is not None:
-        if residual.dtype not in (torch.float32, td):
-            raise ValueError(f"residual has dtype {residual.dtype}, expected float32 or {td}")
-        rcode = _DTYPES[residual.dtype]
-        rp = _dense(residual, "residual", residual.dtype, x.shape, dev)
+        rd = residual.dtype if isinstance(residual, torch.Tensor) else None
+        if rd is not td and rd is not torch.float32:
+            raise ValueError(f"residual has dtype {rd}, expected float32 or {td}")
+        rcode = _DTYPES[rd]
+        rp = _dense(residual, "residual", rd, shape, dev)
         if residual_out is None and want_residual:
-            residual_out = torch.empty(x.shape, device=dev, dtype=residual.dtype)
-        op = _dense(residual_out, "residual_out", residual.dtype, x.shape, dev)
+            residual_out = _empty(shape, rd, x.device)
+        op = _dense(residual_out, "residual_out", rd, shape, dev)
     elif residual_out is not None:
         raise ValueError("residual_out without a residual")
     if y is None:
-        y = torch.empty(x.shape, device=dev, dtype=td)
-    yp = _dense(y, "y", td, x.shape, dev)
-    rows = x.numel() // c if c else 0
-    prob = NormProblem(rows, c, ngroups, x_pitch, z_pitch, eps, scale, int(bool(gate_after)), code,
-                       rcode)
-    _Call(lib().ssd_norm, (ctypes.byref(prob), xp, zp, rp, wp, yp, op, _stream(stream, dev)), dev,
-          "ssd_norm", None)()
+        y = _empty(shape, td, x.device)
+    yp = _dense(y, "y", td, shape, dev)
+    prob = NormProblem(x.numel() // c if c else 0, c, ngroups, x_pitch, z_pitch, eps, scale,
+                       1 if gate_after else 0, code, rcode)
+    _call(lib().ssd_norm, (ctypes.byref(prob), xp, zp, rp, wp, yp, op, _stream(stream, dev)), dev,
+          "ssd_norm")
     return y if residual is None else (y, residual_out)

@@ -249,11 +249,10 @@ def test_binding_refuses_host_tensors():
     ((2, 5, 8), (20, 4, 1), 2, None),     # rows that overlap
     ((6, 8), (0, 1), 1, None),
 ])
-def test_row_layouts(shape, stride, lead, pitch, monkeypatch):
-    monkeypatch.setattr(block, "_check", lambda *a: None)
+def test_row_layouts(shape, stride, lead, pitch):
     t = torch.empty(4096).as_strided(shape, stride)
     if pitch is None:
         with pytest.raises(ValueError):
-            block._rows(t, "t", t.dtype, t.shape, None, lead)
+            block._pitch(t, "t", lead)
     else:
-        assert block._rows(t, "t", t.dtype, t.shape, None, lead)[1] == pitch
+        assert block._pitch(t, "t", lead) == pitch
