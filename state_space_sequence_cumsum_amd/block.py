@@ -90,6 +90,11 @@ def _pitch(t, name, lead):
     """Elements between the tokens of a tensor whose first `lead` dimensions count tokens: the
     others are dense, and the tokens follow each other at one pitch (0: dense tokens)."""
     shape, stride, width = t.shape, t.stride(), 1
+    if lead == 2 and len(shape) == 3 and shape[1] > 1:      # the usual slice, without the loops
+        b, L, c = shape
+        pitch = stride[1]
+        if pitch >= c and (c == 1 or stride[2] == 1) and (b == 1 or stride[0] == L * pitch):
+            return pitch
     for d in range(len(shape) - 1, lead - 1, -1):
         if shape[d] != 1 and stride[d] != width:
             raise ValueError(f"{name} must have dense rows")
@@ -201,7 +206,9 @@ def _conv_args(x, weight, bias, state, silu, lengths, split, y, final_state, wan
     lp = _dense(lengths, "lengths", torch.int32, (b,), dev)
     if final_state is None and want_final:
         final_state = _empty((b, k - 1, c), td, x.device)
-    fp = _dense(final_state, "final_state", td, (b, k - 1, c), dev)
+        fp = final_state.data_ptr()
+    else:
+        fp = _dense(final_state, "final_state", td, (b, k - 1, c), dev)
     args = (ctypes.byref(prob), xp, wp, bp, sp, lp, *yp, fp, _stream(stream, dev))
     return args, dev, out, final_state, None
 
@@ -298,21 +305,26 @@ def ssd_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, *, dt_softpl
     lp = _dense(lengths, "lengths", torch.int32, (prob.batch,), dev)
     if y is None:
         y = _empty(x.shape, td, x.device)
-    yp = _dense(y, "y", td, x.shape, dev)
+        yp = y.data_ptr()
+    else:
+        yp = _dense(y, "y", td, x.shape, dev)
     if hT is None and want_final:
         hT = _empty(states, f32, x.device)
-    tp = _dense(hT, "hT", f32, states, dev)
+        tp = hT.data_ptr()
+    else:
+        tp = _dense(hT, "hT", f32, states, dev)
     L, p = lib(), ctypes.byref(prob)
     if workspace is None:
         n = L.ssd_scan_workspace_bytes(p)
         if n == 0:
             _raise(L.ssd_scan_validate(p), "ssd_scan")
         workspace = _empty(n, torch.uint8, x.device)
-    elif workspace.get_device() != dev or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor on the inputs' device")
-    _call(L.ssd_scan, (p, *ptrs, hp, lp, yp, tp, workspace.data_ptr(),
-                       workspace.numel() * workspace.element_size(), _stream(stream, dev)), dev,
-          "ssd_scan")
+    else:
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on the inputs' device")
+        n = workspace.numel() * workspace.element_size()
+    _call(L.ssd_scan, (p, *ptrs, hp, lp, yp, tp, workspace.data_ptr(), n, _stream(stream, dev)),
+          dev, "ssd_scan")
     return y, hT
 
 
@@ -379,12 +391,16 @@ def ssd_norm(x, weight, z=None, residual=None, *, ngroups=1, eps=1e-5, scale=1.0
         rp = _dense(residual, "residual", rd, shape, dev)
         if residual_out is None and want_residual:
             residual_out = _empty(shape, rd, x.device)
-        op = _dense(residual_out, "residual_out", rd, shape, dev)
+            op = residual_out.data_ptr()
+        else:
+            op = _dense(residual_out, "residual_out", rd, shape, dev)
     elif residual_out is not None:
         raise ValueError("residual_out without a residual")
     if y is None:
         y = _empty(shape, td, x.device)
-    yp = _dense(y, "y", td, shape, dev)
+        yp = y.data_ptr()
+    else:
+        yp = _dense(y, "y", td, shape, dev)
     prob = NormProblem(x.numel() // c if c else 0, c, ngroups, x_pitch, z_pitch, eps, scale,
                        1 if gate_after else 0, code, rcode)
     _call(lib().ssd_norm, (ctypes.byref(prob), xp, zp, rp, wp, yp, op, _stream(stream, dev)), dev,
