@@ -406,15 +406,18 @@ __global__ __launch_bounds__(256) void scan_step_kernel(
 //     2048 tokens: 709 whole, 404 in eight).
 //   - So do sequences under 32 tokens, where two more launches cost more than a walk (16 tokens:
 //     7.8 us whole, 12.0 split; 32 tokens: 13.0 and 12.1).
-//   - Else up to about 4096 waves (one 16384-token sequence of 2048 channels: 231 us with 2048
-//     waves, 210 with 4096, 210 with 6144), in segments of 16 tokens at least, or of 8 where
-//     even these are few (256 tokens, 256 channels: 12.6 us against 16.6).
+//   - Else up to about 8192 waves of at least 32 tokens (one 16384-token sequence of 2048
+//     channels: 231 us with 2048 waves, 209 with 4096, 204 with 8192, 211 with 12288; eight
+//     ragged ones of 2048 tokens: 204 with 4096, 146 with 8192), or 4096 of fewer tokens (four of
+//     2048 tokens, 1024 channels of 32 states: 116 us, 125 with 24 tokens), at least 16, or 8
+//     where even these are few (256 tokens, 256 channels: 12.6 us against 16.6).
 void split_of(const ScanShape &s, int64_t waves, int &S, int &seg)
 {
     int64_t tokens = s.L;
     if (waves < 1024 && s.L >= 32) {
         const int64_t least = waves * s.L <= 8 * 2048 ? 8 : 16;
-        tokens = (waves * s.L + 4095) / 4096;
+        const int64_t fine = (waves * s.L + 8191) / 8192, coarse = (waves * s.L + 4095) / 4096;
+        tokens = fine >= 32 ? fine : coarse < 32 ? coarse : 32;
         if (tokens < least) tokens = least;
     }
     tokens = (tokens + kStep - 1) / kStep * kStep;
