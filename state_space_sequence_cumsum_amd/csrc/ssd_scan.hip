@@ -284,6 +284,12 @@ __global__ __launch_bounds__(64) __attribute__((amdgpu_waves_per_eu(N <= 16 ? 4 
 // A workgroup owns 64 channels and one state; its waves take runs of segments, load them all at
 // once, form each run's own decay and end, and after an exchange through LDS walk their runs
 // from the true start: two trips to memory whatever the number of segments in a round.
+// decay * state + more, where a zero state stays zero under a decay that overflowed (positive
+// rates over a whole segment; token by token nothing would overflow)
+__device__ __forceinline__ float carried(float decay, float state, float more)
+{
+    return state == 0.0f ? more : fmaf(decay, state, more);
+}
 constexpr int kRunWaves = 8, kRun = 16;     // at most: waves of a workgroup, segments of a run
 __global__ __launch_bounds__(64 * kRunWaves) void scan_combine_kernel(const float *__restrict__ A,
                                                                       const float *h0, ScanWs ws,
@@ -322,8 +328,8 @@ __global__ __launch_bounds__(64 * kRunWaves) void scan_combine_kernel(const floa
             const bool on = i < per && first + i < m.S - 1;
             d[i] = on ? fast_exp2(a2 * d[i]) : 1.0f;
             e[i] = on ? e[i] : 0.0f;
-            end = fmaf(d[i], end, e[i]);
-            decay *= d[i];
+            end = carried(d[i], end, e[i]);
+            decay = carried(d[i], decay, 0.0f);
         }
         run_decay[wv][lane] = decay;
         run_end[wv][lane] = end;
@@ -332,13 +338,13 @@ __global__ __launch_bounds__(64 * kRunWaves) void scan_combine_kernel(const floa
 #pragma unroll
         for (int w = 0; w < kRunWaves; ++w) {
             if (w == wv) mine = h;
-            if (w < nw) h = fmaf(run_decay[w][lane], h, run_end[w][lane]);
+            if (w < nw) h = carried(run_decay[w][lane], h, run_end[w][lane]);
         }
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < kRun; ++i) {
             if (i < per && first + i < m.S) st[(int64_t)(first + i) * N * Cw] = mine;
-            mine = fmaf(d[i], mine, e[i]);
+            mine = carried(d[i], mine, e[i]);
         }
     }
 }

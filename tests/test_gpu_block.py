@@ -273,6 +273,21 @@ def test_scan_zero_step_keeps_state_bitwise():
         assert torch.equal(hT, d["h0"])
 
 
+def test_scan_zero_state_under_growing_rates():
+    """Positive rates: a segment's decay overflows, but a state that is still zero stays zero,
+    as it does token by token."""
+    dev = require_gpu()
+    d = _scan_inputs("fp32", 1, 400, 64, 1, 16, dev, 22, h0=False, act=False, bias=False)
+    d["A"] = -d["A"]
+    d["dt"].fill_(1.0)
+    d["x"][:, :-2] = 0
+    y, hT = _run_scan(d, False)
+    torch.cuda.synchronize()
+    ry, ey, rh, eh = _ref_scan(d, False)
+    ref.check(y, ry, ey, "y")
+    ref.check(hT, rh, eh, "hT")
+
+
 def test_scan_repeats_bitwise():
     """No atomics: the same call gives the same bits."""
     dev = require_gpu()
