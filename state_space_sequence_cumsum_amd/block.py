@@ -128,8 +128,15 @@ def _io(x, name="x"):
     return code, x.get_device()
 
 
-def _empty(shape, dtype, device):
-    return torch.empty(shape, dtype=dtype, device=device)
+def _empty(shape, dtype, device, stream):
+    """A new tensor for a call on `stream` (None: the current one): it comes from that stream's
+    memory, which earlier work on the current stream may not be using any more."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _stream(stream, device):
@@ -186,7 +193,7 @@ def _conv_args(x, weight, bias, state, silu, lengths, split, y, final_state, wan
     bp = _dense(bias, "bias", torch.float32, (c,), dev)
     sp = _dense(state, "state", td, (b, k - 1, c), dev)
     if y is None:
-        ys = tuple([_empty((*lead, w), td, x.device) for w in widths])
+        ys = tuple([_empty((*lead, w), td, x.device, stream) for w in widths])
         yp = [t.data_ptr() for t in ys]
     else:
         ys = (y,) if isinstance(y, torch.Tensor) else tuple(y)
@@ -205,7 +212,7 @@ def _conv_args(x, weight, bias, state, silu, lengths, split, y, final_state, wan
         return args, dev, out, state, (x, weight, bias, state, ys)
     lp = _dense(lengths, "lengths", torch.int32, (b,), dev)
     if final_state is None and want_final:
-        final_state = _empty((b, k - 1, c), td, x.device)
+        final_state = _empty((b, k - 1, c), td, x.device, stream)
         fp = final_state.data_ptr()
     else:
         fp = _dense(final_state, "final_state", td, (b, k - 1, c), dev)
@@ -304,12 +311,12 @@ def ssd_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, *, dt_softpl
     hp = _dense(h0, "h0", f32, states, dev)
     lp = _dense(lengths, "lengths", torch.int32, (prob.batch,), dev)
     if y is None:
-        y = _empty(x.shape, td, x.device)
+        y = _empty(x.shape, td, x.device, stream)
         yp = y.data_ptr()
     else:
         yp = _dense(y, "y", td, x.shape, dev)
     if hT is None and want_final:
-        hT = _empty(states, f32, x.device)
+        hT = _empty(states, f32, x.device, stream)
         tp = hT.data_ptr()
     else:
         tp = _dense(hT, "hT", f32, states, dev)
@@ -318,7 +325,7 @@ def ssd_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, *, dt_softpl
         n = L.ssd_scan_workspace_bytes(p)
         if n == 0:
             _raise(L.ssd_scan_validate(p), "ssd_scan")
-        workspace = _empty(n, torch.uint8, x.device)
+        workspace = _empty(n, torch.uint8, x.device, stream)
     else:
         if workspace.get_device() != dev or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on the inputs' device")
@@ -334,7 +341,7 @@ def _scan_step_args(x, dt, A, B, C, h, D, z, dt_bias, dt_softplus, y, stream):
         raise ValueError("h must be a GPU tensor")
     hp = _dense(h, "h", torch.float32, (prob.batch, prob.channels, prob.dstate), dev)
     if y is None:
-        y = _empty(x.shape, x.dtype, x.device)
+        y = _empty(x.shape, x.dtype, x.device, stream)
     yp = _dense(y, "y", x.dtype, x.shape, dev)
     return (ctypes.byref(prob), *ptrs, hp, yp, _stream(stream, dev)), dev, y
 
@@ -390,14 +397,14 @@ def ssd_norm(x, weight, z=None, residual=None, *, ngroups=1, eps=1e-5, scale=1.0
         rcode = _DTYPES[rd]
         rp = _dense(residual, "residual", rd, shape, dev)
         if residual_out is None and want_residual:
-            residual_out = _empty(shape, rd, x.device)
+            residual_out = _empty(shape, rd, x.device, stream)
             op = residual_out.data_ptr()
         else:
             op = _dense(residual_out, "residual_out", rd, shape, dev)
     elif residual_out is not None:
         raise ValueError("residual_out without a residual")
     if y is None:
-        y = _empty(shape, td, x.device)
+        y = _empty(shape, td, x.device, stream)
         yp = y.data_ptr()
     else:
         yp = _dense(y, "y", td, shape, dev)

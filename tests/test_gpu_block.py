@@ -468,6 +468,30 @@ def test_side_stream_and_graph_replays():
             assert all(torch.equal(p, q) for p, q in zip(want, out)), f"replay {rep}"
 
 
+def test_given_stream_gets_its_own_memory():
+    """Outputs and workspaces of a call on a given stream come from that stream's memory, not
+    from what the current stream has just freed and may still be using."""
+    dev = require_gpu()
+    side = torch.cuda.Stream(dev)
+    b, L, c = 1, 4096, 256
+    d = _scan_inputs("bf16", b, L, c, 1, 16, dev, 23)
+    conv = _conv_inputs("bf16", b, L, c, 4, dev, 24)
+    w = torch.ones(c, device=dev)
+    torch.cuda.synchronize()
+    for handle in (side, side.cuda_stream):
+        freed = [torch.empty(b, L, c, device=dev, dtype=torch.bfloat16) for _ in range(8)]
+        freed += [torch.empty(b, c, 16, device=dev) for _ in range(4)]
+        taken = {t.data_ptr() for t in freed}
+        del freed
+        u, cs = ssd.ssd_conv(conv[0], conv[1], stream=handle)
+        y, hT = _run_scan(d, True, stream=handle)
+        o = ssd.ssd_norm(d["x"], w, stream=handle)
+        assert not taken & {t.data_ptr() for t in (u, y, hT, o)}
+        torch.cuda.synchronize()
+        want = ssd.ssd_conv(conv[0], conv[1])[0], *_run_scan(d, True), ssd.ssd_norm(d["x"], w)
+        assert all(torch.equal(p, q) for p, q in zip((u, y, hT, o), want))
+
+
 def test_step_plans_and_graph():
     """ConvStepPlan and ScanStepPlan captured into one decode graph, inputs refilled between
     the replays: the states and outputs of the eager steps, bit for bit."""
