@@ -118,6 +118,17 @@ struct ScanWs {
     float *state, *steps;
 };
 
+// Tokens of sequence b, and how many of its segments these reach (one at least: an empty
+// sequence's first segment hands its initial state on).
+__device__ __forceinline__ int64_t tokens_of(const int32_t *lengths, int64_t b, const ScanDims &m)
+{
+    return lengths ? min((int64_t)max(lengths[b], 0), m.L) : m.L;
+}
+__device__ __forceinline__ int segments_of(int64_t len, const ScanDims &m)
+{
+    return max((int)((len + m.seg - 1) / m.seg), 1);
+}
+
 template <typename T, int N, int KIND>
 __global__ __launch_bounds__(64) __attribute__((amdgpu_waves_per_eu(N <= 16 ? 4 : N <= 32 ? 3 : 2))) void scan_kernel(
     const T *__restrict__ x, const T *__restrict__ dt, const float *__restrict__ A,
@@ -140,8 +151,10 @@ __global__ __launch_bounds__(64) __attribute__((amdgpu_waves_per_eu(N <= 16 ? 4 
     const int in_group = (wave % m.tiles) * 64 + threadIdx.x;
     const bool live = in_group < m.Cg;
     const int c = g * m.Cg + min(in_group, m.Cg - 1);
-    int64_t len = m.L;
-    if (lengths) len = min((int64_t)max(lengths[b], 0), m.L);
+    const int64_t len = tokens_of(lengths, b, m);
+    const int last = segments_of(len, m) - 1;
+    // segments behind the sequence's last one; nothing continues from the last one's end
+    if (KIND == kEnds ? seg >= last : seg > last) return;
     const int64_t t0 = (int64_t)seg * m.seg;
     const int64_t t1 = KIND == kWhole ? len : min(t0 + m.seg, len);
     const int count = (int)max(t1 - t0, (int64_t)0);
@@ -268,7 +281,7 @@ __global__ __launch_bounds__(64) __attribute__((amdgpu_waves_per_eu(N <= 16 ? 4 
 #pragma unroll
         for (int n = 0; n < N; ++n) ws.state[(slot * N + n) * Cw + cw] = h[n];
         ws.steps[slot * Cw + cw] = steps;
-    } else if (hT && live && seg == m.S - 1) {
+    } else if (hT && live && seg == last) {
 #pragma unroll
         for (int n = 0; n < N; n += 4) {
             f32x4 v;
@@ -292,8 +305,9 @@ __device__ __forceinline__ float carried(float decay, float state, float more)
 }
 constexpr int kRunWaves = 8, kRun = 16;     // at most: waves of a workgroup, segments of a run
 __global__ __launch_bounds__(64 * kRunWaves) void scan_combine_kernel(const float *__restrict__ A,
-                                                                      const float *h0, ScanWs ws,
-                                                                      int N, ScanDims m)
+                                                                      const float *h0,
+                                                                      const int32_t *__restrict__ lengths,
+                                                                      ScanWs ws, int N, ScanDims m)
 {
     __shared__ float run_decay[kRunWaves][64], run_end[kRunWaves][64];
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
@@ -309,15 +323,16 @@ __global__ __launch_bounds__(64 * kRunWaves) void scan_combine_kernel(const floa
     float *st = ws.state + (b * m.S * N + n) * Cw + wave * 64 + lane;
     const float *sm = ws.steps + b * m.S * Cw + wave * 64 + lane;
     // segments 0 .. S - 2 have an end state; start states are written for 0 .. S - 1
+    const int S = segments_of(tokens_of(lengths, b, m), m);
     const int nw = blockDim.x >> 6;
-    for (int s0 = 0; s0 < m.S; s0 += nw * kRun) {
-        const int per = min((m.S - s0 + nw - 1) / nw, kRun);
+    for (int s0 = 0; s0 < S; s0 += nw * kRun) {
+        const int per = min((S - s0 + nw - 1) / nw, kRun);
         const int first = s0 + wv * per;
         float e[kRun], d[kRun];
 #pragma unroll
         for (int i = 0; i < kRun; ++i) {
             if (i < per) {
-                const int64_t s = min(first + i, m.S - 2);
+                const int64_t s = min(first + i, max(S - 2, 0));
                 e[i] = st[s * N * Cw];
                 d[i] = sm[s * Cw];
             }
@@ -325,7 +340,7 @@ __global__ __launch_bounds__(64 * kRunWaves) void scan_combine_kernel(const floa
         float decay = 1.0f, end = 0.0f;
 #pragma unroll
         for (int i = 0; i < kRun; ++i) {
-            const bool on = i < per && first + i < m.S - 1;
+            const bool on = i < per && first + i < S - 1;
             d[i] = on ? fast_exp2(a2 * d[i]) : 1.0f;
             e[i] = on ? e[i] : 0.0f;
             end = carried(d[i], end, e[i]);
@@ -343,7 +358,7 @@ __global__ __launch_bounds__(64 * kRunWaves) void scan_combine_kernel(const floa
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < kRun; ++i) {
-            if (i < per && first + i < m.S) st[(int64_t)(first + i) * N * Cw] = mine;
+            if (i < per && first + i < S) st[(int64_t)(first + i) * N * Cw] = mine;
             mine = carried(d[i], mine, e[i]);
         }
     }
@@ -477,7 +492,7 @@ hipError_t scan_go(const ScanShape &s, const ScanArgs &a, float *h, hipStream_t 
     // runs of eight segments or more
     const int run_waves = m.S >= 8 * kRunWaves ? kRunWaves : (m.S + 7) / 8;
     hipLaunchKernelGGL(scan_combine_kernel, dim3((unsigned)(m.G * m.tiles * N * s.b)),
-                       dim3(64 * run_waves), 0, st, a.A, a.h0, ws, N, m);
+                       dim3(64 * run_waves), 0, st, a.A, a.h0, a.lengths, ws, N, m);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
     return scan_pass<T, N, kOut>(s, m, ws, a, st);
