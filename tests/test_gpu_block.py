@@ -100,6 +100,25 @@ def test_conv_in_pieces(dtype, c, k):
     assert torch.equal(torch.cat(parts, 1), y_all) and torch.equal(state, f_all)
 
 
+@pytest.mark.parametrize("dtype,c,split", [("bf16", 2560, [2048, 256, 256]), ("bf16", 1001, [1001]),
+                                           ("fp32", 1024, [1024])])
+def test_conv_token_tiles(dtype, c, split):
+    """Every output is the same sum whichever tile its token falls into: a long prompt (tiles of
+    32 tokens) gives the bits of its pieces (tiles of 8)."""
+    dev = require_gpu()
+    L = 16390
+    x, w, bv, s0 = _conv_inputs(dtype, 1, L, c, 4, dev, 25)
+    ys, f = ssd.ssd_conv(x, w, bv, s0, split=split)
+    state, parts = s0.clone(), []
+    for lo in range(0, L, 1500):
+        y, _ = ssd.ssd_conv(x[:, lo:lo + 1500], w, bv, state, split=split, final_state=state)
+        parts.append(y)
+    torch.cuda.synchronize()
+    for i, y in enumerate(ys):
+        assert torch.equal(y, torch.cat([p[i] for p in parts], 1))
+    assert torch.equal(f, state)
+
+
 @pytest.mark.parametrize("dtype,b,split,k,cols,act,bias", [
     ("bf16", 1, [2048, 256, 256], 4, (2048, 32), True, True),
     ("bf16", 128, [520], 4, (0, 0), True, True),
@@ -175,6 +194,12 @@ SCAN_CASES = [
     ("bf16", 2, 300, 257, 1, 16, {}),
     ("fp32", 1, 700, 64, 1, 16, {}),
     ("bf16", 1, 1025, 192, 1, 16, dict(h0=False)),
+    # every state size split into segments, with odd ends
+    ("bf16", 2, 77, 70, 1, 8, {}),
+    ("fp32", 1, 100, 130, 2, 24, {}),
+    ("bf16", 3, 45, 33, 1, 48, {}),
+    # enough channels for whole walks of a longer sequence
+    ("bf16", 128, 37, 520, 1, 8, {}),
     # step sizes from e^-23 to 17: the far ends of the softplus
     ("fp32", 1, 200, 64, 1, 16, dict(spread=8.0)),
     ("bf16", 2, 90, 64, 1, 8, dict(spread=8.0)),
@@ -343,6 +368,11 @@ NORM_CASES = [
     ("bf16", 300, 96, 1, "first", "fp32", (0, 4)),
     ("bf16", 2, 20001, 1, "first", "bf16", (0, 0)),
     ("fp32", 9, 516, 1, "none", None, (0, 0)),
+    # teams that walk over several rows: waves, workgroups, parts of a wave, three groups
+    ("bf16", 9001, 1024, 1, "first", None, (0, 0)),
+    ("bf16", 2100, 4096, 1, "none", "bf16", (0, 0)),
+    ("fp32", 70003, 32, 1, "after", None, (0, 0)),
+    ("bf16", 4001, 1032, 3, "first", "fp32", (0, 8)),
 ]
 
 
