@@ -112,7 +112,7 @@ __device__ __forceinline__ void buf_store(rsrc_t r, uint32_t off, uint32_t row, 
 constexpr int kStep = 8;    // segments are multiples of this many tokens
 
 // The workspace of a split scan: per (sequence, segment), the state at the segment's end
-// (kEnds) and, after the combination, at its start, as [N][Cw] with Cw = G * tiles * 64, so
+// (kEnds) and, after the chain, at its start, as [N][Cw] with Cw = G * tiles * 64, so
 // that a wave's lanes stand side by side; and the sum of its step sizes [Cw].
 struct ScanWs {
     float *state, *steps;
@@ -292,25 +292,24 @@ __global__ __launch_bounds__(64) __attribute__((amdgpu_waves_per_eu(N <= 16 ? 4 
     }
 }
 
+// exp2(v), finite: under positive rates a segment's decay may overflow where token by token
+// nothing would, and a state that is still zero has to stay zero under it.
+__device__ __forceinline__ float finite_exp2(float v) { return fminf(fast_exp2(v), 3.4028235e38f); }
+
 // Turns the segments' end states (each from zero) into their start states, in place: along
 // the segments, start[0] = h0 and start[s + 1] = exp(A sum of steps of s) start[s] + end[s].
 // A workgroup owns 64 channels and one state; its waves take runs of segments, load them all at
 // once, form each run's own decay and end, and after an exchange through LDS walk their runs
 // from the true start: two trips to memory whatever the number of segments in a round.
-// decay * state + more, where a zero state stays zero under a decay that overflowed (positive
-// rates over a whole segment; token by token nothing would overflow)
-__device__ __forceinline__ float carried(float decay, float state, float more)
-{
-    return state == 0.0f ? more : fmaf(decay, state, more);
-}
+// Wave, segments and their addresses are scalars; a lane adds its channel.
 constexpr int kRunWaves = 8, kRun = 16;     // at most: waves of a workgroup, segments of a run
-__global__ __launch_bounds__(64 * kRunWaves) void scan_combine_kernel(const float *__restrict__ A,
-                                                                      const float *h0,
-                                                                      const int32_t *__restrict__ lengths,
-                                                                      ScanWs ws, int N, ScanDims m)
+__global__ __launch_bounds__(64 * kRunWaves) void scan_chain_kernel(
+    const float *__restrict__ A, const float *h0, const int32_t *__restrict__ lengths, ScanWs ws,
+    int N, ScanDims m)
 {
     __shared__ float run_decay[kRunWaves][64], run_end[kRunWaves][64];
-    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+    const uint32_t lane = threadIdx.x & 63;
+    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int gt = m.G * m.tiles;
     const int wave = blockIdx.x % gt, n = blockIdx.x / gt % N;
     const int64_t b = blockIdx.x / gt / N;
@@ -320,46 +319,45 @@ __global__ __launch_bounds__(64 * kRunWaves) void scan_combine_kernel(const floa
     const int c = wave / m.tiles * m.Cg + min(in_group, m.Cg - 1);
     const float a2 = kLog2e * A[(int64_t)c * N + n];
     float h = h0 && live ? h0[(b * m.C + c) * N + n] : 0.0f;
-    float *st = ws.state + (b * m.S * N + n) * Cw + wave * 64 + lane;
-    const float *sm = ws.steps + b * m.S * Cw + wave * 64 + lane;
+    float *st = ws.state + (b * m.S * N + n) * Cw + wave * 64;
+    const float *sm = ws.steps + b * m.S * Cw + wave * 64;
     // segments 0 .. S - 2 have an end state; start states are written for 0 .. S - 1
     const int S = segments_of(tokens_of(lengths, b, m), m);
     const int nw = blockDim.x >> 6;
     for (int s0 = 0; s0 < S; s0 += nw * kRun) {
         const int per = min((S - s0 + nw - 1) / nw, kRun);
         const int first = s0 + wv * per;
+        const int starts = min(per, S - first), ends = min(per, S - 1 - first);
         float e[kRun], d[kRun];
 #pragma unroll
         for (int i = 0; i < kRun; ++i) {
-            if (i < per) {
-                const int64_t s = min(first + i, max(S - 2, 0));
-                e[i] = st[s * N * Cw];
-                d[i] = sm[s * Cw];
+            if (i < ends) {
+                e[i] = (st + (int64_t)(first + i) * N * Cw)[lane];
+                d[i] = (sm + (first + i) * Cw)[lane];
             }
         }
         float decay = 1.0f, end = 0.0f;
 #pragma unroll
         for (int i = 0; i < kRun; ++i) {
-            const bool on = i < per && first + i < S - 1;
-            d[i] = on ? fast_exp2(a2 * d[i]) : 1.0f;
-            e[i] = on ? e[i] : 0.0f;
-            end = carried(d[i], end, e[i]);
-            decay = carried(d[i], decay, 0.0f);
+            if (i < ends) {
+                d[i] = finite_exp2(a2 * d[i]);
+                end = fmaf(d[i], end, e[i]);
+                decay = fminf(decay * d[i], 3.4028235e38f);
+            }
         }
         run_decay[wv][lane] = decay;
         run_end[wv][lane] = end;
         __syncthreads();
         float mine = h;
-#pragma unroll
-        for (int w = 0; w < kRunWaves; ++w) {
+        for (int w = 0; w < nw; ++w) {
             if (w == wv) mine = h;
-            if (w < nw) h = carried(run_decay[w][lane], h, run_end[w][lane]);
+            h = fmaf(run_decay[w][lane], h, run_end[w][lane]);
         }
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < kRun; ++i) {
-            if (i < per && first + i < S) st[(int64_t)(first + i) * N * Cw] = mine;
-            mine = carried(d[i], mine, e[i]);
+            if (i < starts) (st + (int64_t)(first + i) * N * Cw)[lane] = mine;
+            if (i < ends) mine = fmaf(d[i], mine, e[i]);
         }
     }
 }
@@ -489,10 +487,14 @@ hipError_t scan_go(const ScanShape &s, const ScanArgs &a, float *h, hipStream_t 
     if (m.S == 1) return scan_pass<T, N, kWhole>(s, m, ws, a, st);
     hipError_t e = scan_pass<T, N, kEnds>(s, m, ws, a, st);
     if (e != hipSuccess) return e;
-    // runs of eight segments or more
-    const int run_waves = m.S >= 8 * kRunWaves ? kRunWaves : (m.S + 7) / 8;
-    hipLaunchKernelGGL(scan_combine_kernel, dim3((unsigned)(m.G * m.tiles * N * s.b)),
-                       dim3(64 * run_waves), 0, st, a.A, a.h0, a.lengths, ws, N, m);
+    // Waves of a chain workgroup: runs of eight segments where there are few workgroups (32768
+    // tokens of 512 channels: 130 us, 141 with runs of sixteen), else of sixteen (four sequences
+    // of 2048 tokens, 2048 channels: 115 us against 121)
+    const int64_t chains = (int64_t)m.G * m.tiles * N * s.b;
+    const int least = chains < 1024 ? 8 : 16;
+    const int run_waves = m.S >= least * kRunWaves ? kRunWaves : (m.S + least - 1) / least;
+    hipLaunchKernelGGL(scan_chain_kernel, dim3((unsigned)chains), dim3(64 * run_waves), 0, st, a.A,
+                       a.h0, a.lengths, ws, N, m);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
     return scan_pass<T, N, kOut>(s, m, ws, a, st);
