@@ -10,8 +10,8 @@
 // 32, from the caches).  2 K + 5 flops an element: HBM bound.  Three outputs, so that the x, B
 // and C columns of a block's projection come out as ssd_forward takes them.
 //
-// Measured (inputs not in the caches): 16384 x 2560 bf16, a slice of rows of 4640, 41.2 us
-// (4.1 TB/s; a 1 GiB copy reaches 5.1), 262144 x 1536 bf16 299 us (5.4 TB/s), 5 x 2500 x 777
+// Measured (inputs not in the caches): 16384 x 2560 bf16, a slice of rows of 4640, 39 to 41 us
+// (4.2 TB/s; a 1 GiB copy reaches 5.1), 262144 x 1536 bf16 299 us (5.4 TB/s), 5 x 2500 x 777
 // bf16 one channel a thread 15.0 us (2.6 TB/s); 256 x 384 fp32 4.2 us, most of it the launch.
 
 #include <hip/hip_runtime.h>

@@ -14,9 +14,10 @@
 // steps is its decay), and one scans the segments again from there.  The first scan costs 0.8
 // of the second, and the bound is both.
 //
-// Measured (bf16, 16384 tokens, 2048 channels, 16 states, gate and softplus): 210 to 218 us (99
-// and 112 us for the scans, 4 to 5 us for the chain); the VALU slots of both scans are 198 us at
-// the 1.96 ns a slot and wave that an fma loop reaches, HBM's floor is 53 us.  One whole walk per channel: 5.3 ms.
+// Measured (bf16, 16384 tokens, 2048 channels, 16 states, gate and softplus): 207 us (100, 16
+// and 125 us for the two scans and the chain, each profiled by itself); the VALU slots of the two
+// scans are 223 us at the 2.04 GHz of an fma loop, HBM's floor is 53 us.  One whole walk per
+// channel: 5.3 ms.
 
 #include <hip/hip_runtime.h>
 
