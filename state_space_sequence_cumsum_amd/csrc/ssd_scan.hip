@@ -12,7 +12,7 @@
 // tokens are split into segments: one launch scans each segment from zero for its end state, a
 // short one chains these into the segments' start states (exp of A times a segment's summed
 // steps is its decay), and one scans the segments again from there.  The first scan costs 0.8
-// of the second, and the bound is both.
+// of the second, and the bound is both.  Short prompts do the same within one workgroup and launch.
 //
 // Measured (bf16, 16384 tokens, 2048 channels, 16 states, gate and softplus): 207 us (100, 16
 // and 125 us for the two scans and the chain, each profiled by itself); the VALU slots of the two
@@ -363,6 +363,173 @@ __global__ __launch_bounds__(64 * kRunWaves) void scan_chain_kernel(
     }
 }
 
+// ---------------------------------------------------------------------------
+// Short prompts in one launch.  A workgroup owns 16 channels of one group, a wave of it
+// kShort tokens; within a wave four lanes share a channel, N / 4 states each, so that few
+// channels still spread over the card.  Inputs and outputs are loaded and stored with a lane for
+// one channel of four tokens, which also forms their softplus and gates, and change places
+// with the walk's layout through LDS.  Every wave walks its tokens from zero; the waves then
+// share the chain of these ends, each taking some of the states, and walk again from their
+// starts with the outputs.
+// ---------------------------------------------------------------------------
+constexpr int kShort = 16;       // tokens of a wave
+constexpr int kShortCh = 16;     // channels of a workgroup
+
+template <typename T, int N, int kWaves>
+__global__ __launch_bounds__(64 * kWaves) void scan_short_kernel(
+    const T *__restrict__ x, const T *__restrict__ dt, const float *__restrict__ A,
+    const T *__restrict__ B, const T *__restrict__ Cm, const float *__restrict__ D,
+    const T *__restrict__ z, const float *__restrict__ dt_bias, const float *h0,
+    const int32_t *__restrict__ lengths, T *__restrict__ y, float *hT, ScanDims m)
+{
+    constexpr int kOwn = N / 4;                          // states of a lane
+    constexpr int kRow = 2 * N, kQuads = kShort * kRow / 4, kPer = kQuads / 64;
+    __shared__ __attribute__((aligned(16))) float bcs[kWaves][kShort * kRow];
+    __shared__ float2 dus[kWaves][kShort][kShortCh];     // step d, d x
+    __shared__ float ys[kWaves][kShort][kShortCh];
+    __shared__ float ends[kWaves][kOwn][64], sums[kWaves][kShortCh];
+    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63;
+    const int tiles = (m.Cg + kShortCh - 1) / kShortCh;
+    const int tile = blockIdx.x % tiles, g = blockIdx.x / tiles % m.G;
+    const int64_t b = blockIdx.x / tiles / m.G;
+    const int first = g * m.Cg + tile * kShortCh, most = g * m.Cg + m.Cg - 1;
+    const int64_t len = tokens_of(lengths, b, m);
+    const int t0 = wv * kShort;
+    const int count = min(max((int)len - t0, 0), kShort);
+    const int64_t row0 = b * m.L + t0;
+
+    // the walk's layout: channel lane / 4, states part * kOwn ...
+    const int ch = lane >> 2, part = lane & 3;
+    const int c = min(first + ch, most);
+    float a2[kOwn], h[kOwn];
+#pragma unroll
+    for (int k = 0; k < kOwn; ++k) {
+        a2[k] = kLog2e * A[(int64_t)c * N + part * kOwn + k];
+        h[k] = 0.0f;
+    }
+    // the inputs' layout: channel lane % 16, tokens lane / 16 + 4 j
+    const int ic = min(first + (lane & 15), most), it = lane >> 4;
+    const bool live = first + (lane & 15) <= most;
+    float xv[kShort / 4], zv[kShort / 4];
+    if (count > 0) {
+        Quad<T> q[kPer];
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+            const int i = lane + 64 * j;
+            const int64_t r = row0 + min(i / (kRow / 4), count - 1);
+            const int n = i % (kRow / 4) * 4;
+            q[j].load(n < N ? B + r * m.Bp + g * N + n : Cm + r * m.Cp + g * N + (n - N));
+        }
+        float dv[kShort / 4];
+#pragma unroll
+        for (int j = 0; j < kShort / 4; ++j) {
+            const int64_t r = row0 + min(it + 4 * j, count - 1);
+            xv[j] = (float)x[r * m.xp + ic];
+            dv[j] = (float)dt[r * m.dtp + ic];
+            zv[j] = z ? (float)z[r * m.zp + ic] : 0.0f;
+        }
+        const float bias = dt_bias ? dt_bias[ic] : 0.0f;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j)
+            *reinterpret_cast<f32x4 *>(&bcs[wv][4 * (lane + 64 * j)]) = q[j].get();
+#pragma unroll
+        for (int j = 0; j < kShort / 4; ++j) {
+            float d = dv[j] + bias;
+            if (m.sp) d = softplus(d);
+            dus[wv][it + 4 * j][lane & 15] = make_float2(d, d * xv[j]);
+        }
+    }
+    auto states = [&](int i, int at, float *v) {         // kOwn values of B (at 0) or C (at N)
+        const float *p = &bcs[wv][i * kRow + at + part * kOwn];
+#pragma unroll
+        for (int k = 0; k < kOwn; ++k) v[k] = p[k];
+    };
+    const int nw = blockDim.x >> 6;
+    if (nw == 1) {
+        // one wave starts from h0 itself
+#pragma unroll
+        for (int k = 0; k < kOwn; ++k)
+            if (h0) h[k] = h0[(b * m.C + c) * N + part * kOwn + k];
+    } else {
+        float sum = 0.0f;
+#pragma unroll 4
+        for (int i = 0; i < count; ++i) {
+            const float2 du = dus[wv][i][ch];
+            float bv[kOwn];
+            states(i, 0, bv);
+#pragma unroll
+            for (int k = 0; k < kOwn; ++k)
+                h[k] = fmaf(du.y, bv[k], fast_exp2(du.x * a2[k]) * h[k]);
+            sum += du.x;
+        }
+#pragma unroll
+        for (int k = 0; k < kOwn; ++k) ends[wv][k][lane] = h[k];
+        if (part == 0) sums[wv][ch] = sum;
+        __syncthreads();
+        for (int k = wv; k < kOwn; k += nw) {
+            const float rate = kLog2e * A[(int64_t)c * N + part * kOwn + k];
+            float now = h0 ? h0[(b * m.C + c) * N + part * kOwn + k] : 0.0f;
+            float e[kWaves], d[kWaves];
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) {
+                if (w < nw) {
+                    e[w] = ends[w][k][lane];
+                    d[w] = finite_exp2(rate * sums[w][ch]);
+                }
+            }
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) {
+                if (w < nw) {
+                    ends[w][k][lane] = now;
+                    now = fmaf(d[w], now, e[w]);
+                }
+            }
+        }
+        __syncthreads();               // (h0 has been read: a wave may now write hT over it)
+#pragma unroll
+        for (int k = 0; k < kOwn; ++k) h[k] = ends[wv][k][lane];
+    }
+    auto token = [&](int i) {
+        const float2 du = dus[wv][i][ch];
+        float bv[kOwn], cv[kOwn], acc = 0.0f;
+        states(i, 0, bv);
+        states(i, N, cv);
+#pragma unroll
+        for (int k = 0; k < kOwn; ++k) {
+            h[k] = fmaf(du.y, bv[k], fast_exp2(du.x * a2[k]) * h[k]);
+            acc = fmaf(cv[k], h[k], acc);
+        }
+        acc += dpp_move<0xb1, 0xf>(acc);     // quad_perm 1 0 3 2
+        acc += dpp_move<0x4e, 0xf>(acc);     // quad_perm 2 3 0 1
+        if (part == 0) ys[wv][i][ch] = acc;
+    };
+    // (four at a time by hand: the lane moves keep the compiler from it)
+    int i0 = 0;
+    for (; i0 + 4 <= count; i0 += 4) {
+        token(i0);
+        token(i0 + 1);
+        token(i0 + 2);
+        token(i0 + 3);
+    }
+    for (; i0 < count; ++i0) token(i0);
+    const float Dv = D ? D[ic] : 0.0f;
+#pragma unroll
+    for (int j = 0; j < kShort / 4; ++j) {
+        const int i = it + 4 * j;
+        if (i < count && live) {
+            float v = fmaf(Dv, xv[j], ys[wv][i][lane & 15]);
+            if (z) v *= silu(zv[j]);
+            y[(row0 + i) * m.C + ic] = Elem<T>::from_f32(v);
+        }
+    }
+    // the wave of the sequence's last token (the first wave of an empty sequence)
+    if (hT && wv == max((int)((len + kShort - 1) / kShort), 1) - 1 && first + ch <= most) {
+#pragma unroll
+        for (int k = 0; k < kOwn; ++k) hT[(b * m.C + c) * N + part * kOwn + k] = h[k];
+    }
+}
+
 // One token.  The state is read and written once, 8 bytes a state element: HBM bound, latency
 // bound for few sequences.  kLanes lanes, the largest power of two that divides N / 4, share a
 // channel, so that neighbouring lanes hold neighbouring 16 bytes of the state.  128 sequences of
@@ -430,7 +597,7 @@ __global__ __launch_bounds__(256) void scan_step_kernel(
 //     channels: 231 us with 2048 waves, 209 with 4096, 204 with 8192, 211 with 12288; eight
 //     ragged ones of 2048 tokens: 204 with 4096, 146 with 8192), or 4096 of fewer tokens (four of
 //     2048 tokens, 1024 channels of 32 states: 116 us, 125 with 24 tokens), at least 16, or 8
-//     where even these are few (256 tokens, 256 channels: 12.6 us against 16.6).
+//     where even these are few (512 tokens, 512 channels: 13.9 us against 17.2).
 void split_of(const ScanShape &s, int64_t waves, int &S, int &seg)
 {
     int64_t tokens = s.L;
@@ -458,6 +625,34 @@ ScanDims dims_of(const ScanShape &s)
 
 int64_t waves_of(const ScanShape &s, const ScanDims &m) { return (int64_t)m.tiles * m.G * s.b; }
 
+// Waves of a workgroup where the scan runs as one launch, else 0: what one workgroup's LDS holds
+// (16 waves of 16 tokens, 8 for more than 32 states), up to 4096 waves.  One launch and segments,
+// in us: 64 tokens x 2048 channels x 16 states 7.5 and 12.4, 256 x 256 11.5 and 12.6, 128 x 512 x
+// 64 states 17.7 and 24.5; a single token 3.7 and (whole walks) 3.7, 16 tokens 5.5 and 8.0; at
+// 8192 waves (4 x 256 x 2048) 28.7 and 27.1.
+int short_waves(const ScanShape &s, int64_t N)
+{
+    constexpr int64_t kMost = 4096;
+    const int64_t waves = (s.L + kShort - 1) / kShort;
+    const int64_t groups = s.b * s.G * ((s.C / s.G + kShortCh - 1) / kShortCh);
+    return waves <= (N <= 32 ? 16 : 8) && waves * groups <= kMost ? (int)waves : 0;
+}
+
+template <typename T, int N>
+hipError_t scan_short(const ScanShape &s, const ScanDims &m, const ScanArgs &a, hipStream_t st)
+{
+    const int waves = short_waves(s, N);
+    const dim3 grid((unsigned)(s.b * s.G * ((m.Cg + kShortCh - 1) / kShortCh)));
+#define SSD_SHORT(W)                                                                              \
+    hipLaunchKernelGGL((scan_short_kernel<T, N, W>), grid, dim3(64 * waves), 0, st,               \
+                       (const T *)a.x, (const T *)a.dt, a.A, (const T *)a.B, (const T *)a.C, a.D, \
+                       (const T *)a.z, a.dt_bias, a.h0, a.lengths, (T *)a.y, a.hT, m)
+    if (waves <= 4) SSD_SHORT(4);
+    else SSD_SHORT((N <= 32 ? 16 : 8));
+#undef SSD_SHORT
+    return hipGetLastError();
+}
+
 template <typename T, int N, int KIND>
 hipError_t scan_pass(const ScanShape &s, const ScanDims &m, const ScanWs &ws, const ScanArgs &a,
                      hipStream_t st)
@@ -481,6 +676,7 @@ hipError_t scan_go(const ScanShape &s, const ScanArgs &a, float *h, hipStream_t 
                            a.D, (const T *)a.z, a.dt_bias, h, (T *)a.y, m, threads);
         return hipGetLastError();
     }
+    if (short_waves(s, N) > 0) return scan_short<T, N>(s, m, a, st);
     const int64_t Cw = (int64_t)m.G * m.tiles * 64;
     ScanWs ws;
     ws.state = (float *)a.ws;
@@ -522,7 +718,7 @@ hipError_t scan_by_state(const ScanShape &s, const ScanArgs &a, float *h, hipStr
 size_t scan_workspace_bytes(const ScanShape &s)
 {
     const ScanDims m = dims_of(s);
-    if (m.S == 1) return 256;
+    if (m.S == 1 || short_waves(s, s.N) > 0) return 256;
     return (size_t)s.b * m.S * (s.N + 1) * m.G * m.tiles * 64 * sizeof(float);
 }
 

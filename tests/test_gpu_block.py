@@ -198,8 +198,17 @@ SCAN_CASES = [
     ("bf16", 2, 77, 70, 1, 8, {}),
     ("fp32", 1, 100, 130, 2, 24, {}),
     ("bf16", 3, 45, 33, 1, 48, {}),
+    ("bf16", 1, 280, 70, 1, 24, {}),
+    ("fp32", 1, 150, 40, 1, 40, {}),
+    ("bf16", 1, 140, 66, 2, 48, {}),
+    ("fp32", 1, 131, 33, 1, 56, {}),
     # enough channels for whole walks of a longer sequence
     ("bf16", 128, 37, 520, 1, 8, {}),
+    ("fp32", 64, 33, 1024, 2, 16, {}),
+    # one wave, a whole last wave, one token in the last wave of a short prompt
+    ("fp32", 2, 16, 17, 1, 16, dict(h0=False)),
+    ("bf16", 1, 256, 50, 2, 16, {}),
+    ("bf16", 1, 241, 31, 1, 32, dict(z=False, D=False)),
     # step sizes from e^-23 to 17: the far ends of the softplus
     ("fp32", 1, 200, 64, 1, 16, dict(spread=8.0)),
     ("bf16", 2, 90, 64, 1, 8, dict(spread=8.0)),
@@ -268,7 +277,7 @@ def test_scan_column_slices(dtype):
 def test_scan_state_in_place_and_continued():
     """hT in h0's own buffer, and a prompt in two calls and then steps: the whole prompt's."""
     dev = require_gpu()
-    for L, cut in ((90, 37), (1500, 1200)):
+    for L, cut in ((25, 3), (90, 37), (1500, 1200)):
         d = _scan_inputs("fp32", 2, L, 80, 1, 16, dev, 8)
         ry, ey, rh, eh = _ref_scan(d, True)
         h = d["h0"].clone()
@@ -290,7 +299,7 @@ def test_scan_state_in_place_and_continued():
 
 def test_scan_zero_step_keeps_state_bitwise():
     dev = require_gpu()
-    for L in (5, 2000):
+    for L in (5, 100, 2000):
         d = _scan_inputs("fp32", 1, L, 64, 1, 16, dev, 9, act=False, bias=False)
         d["dt"].zero_()
         _, hT = _run_scan(d, False)
@@ -298,11 +307,12 @@ def test_scan_zero_step_keeps_state_bitwise():
         assert torch.equal(hT, d["h0"])
 
 
-def test_scan_zero_state_under_growing_rates():
+@pytest.mark.parametrize("L", [200, 400])
+def test_scan_zero_state_under_growing_rates(L):
     """Positive rates: a segment's decay overflows, but a state that is still zero stays zero,
     as it does token by token."""
     dev = require_gpu()
-    d = _scan_inputs("fp32", 1, 400, 64, 1, 16, dev, 22, h0=False, act=False, bias=False)
+    d = _scan_inputs("fp32", 1, L, 64, 1, 16, dev, 22, h0=False, act=False, bias=False)
     d["A"] = -d["A"]
     d["dt"].fill_(1.0)
     d["x"][:, :-2] = 0
@@ -311,6 +321,16 @@ def test_scan_zero_state_under_growing_rates():
     ry, ey, rh, eh = _ref_scan(d, False)
     ref.check(y, ry, ey, "y")
     ref.check(hT, rh, eh, "hT")
+
+
+def test_scan_without_final_state():
+    dev = require_gpu()
+    for L in (1, 20, 200, 1300):
+        d = _scan_inputs("bf16", 2, L, 130, 1, 16, dev, 26)
+        y0, hT = _run_scan(d, True)
+        y1, none = _run_scan(d, True, want_final=False)
+        torch.cuda.synchronize()
+        assert hT is not None and none is None and torch.equal(y0, y1)
 
 
 def test_scan_repeats_bitwise():
