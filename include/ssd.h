@@ -371,13 +371,17 @@ typedef struct {
  * batch < 2^20 else SSD_ERR_UNSUPPORTED. */
 ssd_status ssd_scan_validate(const ssd_scan_problem *problem);
 
-/* Bytes of device workspace ssd_scan needs; 0 if `problem` is not valid.  Host-only. */
+/* Bytes of device workspace ssd_scan needs; 0 if `problem` is not valid.  Host-only.  Up to
+ * SSD_SCAN_NO_WORKSPACE means none (short prompts, and channels enough for a wave each): the
+ * workspace may then be NULL. */
+#define SSD_SCAN_NO_WORKSPACE 1u
 size_t ssd_scan_workspace_bytes(const ssd_scan_problem *problem);
 
 /* The scan over whole prompts.  x, dt, z, y [b,L,channels] and B, C [b,L,ngroups,dstate] in
  * `dtype`; A [channels, dstate], D and dt_bias [channels] float32; h0, hT [b, channels,
  * dstate] float32, which may be one buffer.  D, z, dt_bias, h0, lengths and hT may be NULL.
- * A, h0, hT and the workspace start on 16 bytes, B and C on 4 bytes with even pitches for
+ * The workspace holds end and start states of segments of long prompts and nothing between
+ * calls.  A, h0, hT and the workspace start on 16 bytes, B and C on 4 bytes with even pitches for
  * SSD_BF16, else SSD_ERR_MISALIGNED. */
 ssd_status ssd_scan(const ssd_scan_problem *problem, const void *x, const void *dt,
                     const float *A, const void *B, const void *C, const float *D, const void *z,

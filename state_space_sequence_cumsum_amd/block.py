@@ -15,6 +15,7 @@ import torch
 from . import binding
 from .binding import SSD_BF16, SSD_F32, _raise
 
+NO_WORKSPACE = 1    # SSD_SCAN_NO_WORKSPACE: a scan that needs up to this many bytes needs none
 _DTYPES = {torch.float32: SSD_F32, torch.bfloat16: SSD_BF16}
 
 
@@ -184,7 +185,7 @@ def _conv_args(x, weight, bias, state, silu, lengths, split, y, final_state, wan
         raise ValueError("weight must be [channels, width]")
     b, c, k = shape[0], shape[-1], weight.shape[1]
     lead = tuple(shape[:-1])
-    widths = (c,) if split is None else tuple(split)
+    widths = (c,) if split is None else tuple([int(w) for w in split])
     n = len(widths)
     if not 1 <= n <= 3 or sum(widths) != c or min(widths) <= 0:
         raise ValueError(f"split {list(widths)} must be 1 to 3 positive widths with sum {c}")
@@ -291,7 +292,7 @@ def scan_problem(x, B, *, dt_softplus=False) -> ScanProblem:
 
 
 def ssd_scan_workspace_bytes(problem: ScanProblem) -> int:
-    """Bytes of workspace ssd_scan needs; 0 when the problem is not valid."""
+    """Bytes of workspace ssd_scan needs (1: none); 0 when the problem is not valid."""
     return lib().ssd_scan_workspace_bytes(ctypes.byref(problem))
 
 
@@ -325,13 +326,14 @@ def ssd_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, *, dt_softpl
         n = L.ssd_scan_workspace_bytes(p)
         if n == 0:
             _raise(L.ssd_scan_validate(p), "ssd_scan")
-        workspace = _empty(n, torch.uint8, x.device, stream)
+        if n > NO_WORKSPACE:
+            workspace = _empty(n, torch.uint8, x.device, stream)
     else:
         if workspace.get_device() != dev or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on the inputs' device")
         n = workspace.numel() * workspace.element_size()
-    _call(L.ssd_scan, (p, *ptrs, hp, lp, yp, tp, workspace.data_ptr(), n, _stream(stream, dev)),
-          dev, "ssd_scan")
+    _call(L.ssd_scan, (p, *ptrs, hp, lp, yp, tp, None if workspace is None else workspace.data_ptr(),
+                       n, _stream(stream, dev)), dev, "ssd_scan")
     return y, hT
 
 

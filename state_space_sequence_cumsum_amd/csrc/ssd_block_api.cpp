@@ -185,7 +185,8 @@ ssd_status ssd_scan(const ssd_scan_problem *problem, const void *x, const void *
     if (st != SSD_OK) return st;
     if (!x || !dt || !A || !B || !C || !y) return SSD_ERR_NULL_ARG;
     const ssd::ScanShape s = scan_shape(problem);
-    if (workspace == nullptr || workspace_bytes < ssd::scan_workspace_bytes(s))
+    const size_t need = ssd::scan_workspace_bytes(s);
+    if (need > SSD_SCAN_NO_WORKSPACE && (workspace == nullptr || workspace_bytes < need))
         return SSD_ERR_WORKSPACE;
     st = check_scan_pointers(problem, A, B, C, {h0, hT, workspace});
     if (st != SSD_OK) return st;

@@ -21,6 +21,7 @@
 
 #include <hip/hip_runtime.h>
 
+#include "../../include/ssd.h"
 #include "ssd_device.h"
 #include "ssd_launch.h"
 
@@ -718,7 +719,7 @@ hipError_t scan_by_state(const ScanShape &s, const ScanArgs &a, float *h, hipStr
 size_t scan_workspace_bytes(const ScanShape &s)
 {
     const ScanDims m = dims_of(s);
-    if (m.S == 1 || short_waves(s, s.N) > 0) return 256;
+    if (m.S == 1 || short_waves(s, s.N) > 0) return SSD_SCAN_NO_WORKSPACE;
     return (size_t)s.b * m.S * (s.N + 1) * m.G * m.tiles * 64 * sizeof(float);
 }
 

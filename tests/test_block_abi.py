@@ -145,8 +145,14 @@ def test_scan_pointer_checks():
         a = [OK16] * 13
         a[missing] = None
         assert L.ssd_scan(ctypes.byref(p), *a, n, None) == 1
-    assert L.ssd_scan(ctypes.byref(p), *[OK16] * 13, n - 1, None) == 4
-    assert L.ssd_scan(ctypes.byref(p), *[OK16] * 12, None, n, None) == 4
+    # short prompts and whole walks take no workspace; segments do
+    assert n == 1 and ssd.ssd_scan_workspace_bytes(_scan(batch=512)) == 1
+    assert "#define SSD_SCAN_NO_WORKSPACE 1u" in open(binding.HEADER).read()
+    long = _scan(seqlen=1000)
+    n = ssd.ssd_scan_workspace_bytes(long)
+    assert n > 1000
+    assert L.ssd_scan(ctypes.byref(long), *[OK16] * 13, n - 1, None) == 4
+    assert L.ssd_scan(ctypes.byref(long), *[OK16] * 12, None, n, None) == 4
     for off, ptr in ((2, OFF4), (8, OFF4), (11, OFF4), (12, OFF4), (3, OFF2), (4, OFF2)):
         a = [OK16] * 13
         a[off] = ptr
