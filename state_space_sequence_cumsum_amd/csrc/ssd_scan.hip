@@ -594,18 +594,22 @@ __global__ __launch_bounds__(256) void scan_step_kernel(
 //     2048 tokens: 709 whole, 404 in eight).
 //   - So do sequences under 32 tokens, where two more launches cost more than a walk (16 tokens:
 //     7.8 us whole, 12.0 split; 32 tokens: 13.0 and 12.1).
-//   - Else up to about 8192 waves of at least 32 tokens (one 16384-token sequence of 2048
-//     channels: 231 us with 2048 waves, 209 with 4096, 204 with 8192, 211 with 12288; eight
-//     ragged ones of 2048 tokens: 204 with 4096, 146 with 8192), or 4096 of fewer tokens (four of
-//     2048 tokens, 1024 channels of 32 states: 116 us, 125 with 24 tokens), at least 16, or 8
-//     where even these are few (512 tokens, 512 channels: 13.9 us against 17.2).
+//   - Else up to about 16384 waves of at least 64 tokens (30 ragged sequences of 1000 tokens, 2048
+//     channels: 220 us, 252 with 8192; dense 380 and 385), or 8192 of at least 32 (one
+//     16384-token sequence of 2048 channels: 231 us with 2048 waves, 209 with 4096, 204 with
+//     8192, 214 to 219 with 16384; eight ragged ones of 2048 tokens: 204 with 4096, 146 with
+//     8192), or 4096 of fewer tokens (four of 2048 tokens, 1024 channels of 32 states: 116 us,
+//     125 with 24 tokens), at least 16, or 8 where even these are few (512 tokens, 512 channels: 13.9 us against 17.2).
 void split_of(const ScanShape &s, int64_t waves, int &S, int &seg)
 {
     int64_t tokens = s.L;
     if (waves < 1024 && s.L >= 32) {
         const int64_t least = waves * s.L <= 8 * 2048 ? 8 : 16;
-        const int64_t fine = (waves * s.L + 8191) / 8192, coarse = (waves * s.L + 4095) / 4096;
-        tokens = fine >= 32 ? fine : coarse < 32 ? coarse : 32;
+        const auto share = [&](int64_t n) { return (waves * s.L + n - 1) / n; };
+        tokens = share(16384) >= 64 ? share(16384)
+                 : share(8192) >= 32 ? (share(8192) < 64 ? share(8192) : 64)
+                 : share(4096) < 32  ? share(4096)
+                                     : 32;
         if (tokens < least) tokens = least;
     }
     tokens = (tokens + kStep - 1) / kStep * kStep;
