@@ -365,43 +365,43 @@ __global__ __launch_bounds__(64 * kRunWaves) void scan_chain_kernel(
 }
 
 // ---------------------------------------------------------------------------
-// Short prompts in one launch.  A workgroup owns 16 channels of one group, a wave of it
-// kShort tokens; within a wave four lanes share a channel, N / 4 states each, so that few
-// channels still spread over the card.  Inputs and outputs are loaded and stored with a lane for
-// one channel of four tokens, which also forms their softplus and gates, and change places
-// with the walk's layout through LDS.  Every wave walks its tokens from zero; the waves then
+// Short prompts in one launch.  A workgroup owns 64 / kLanes channels of one group, a wave of
+// it kShort tokens; within a wave kLanes (4 or 8) lanes share a channel, N / kLanes states each,
+// so that few channels still spread over the card.  Inputs and outputs are loaded and stored
+// with a lane for one channel of a few tokens, which also forms their softplus and gates, and
+// change places with the walk's layout through LDS.  Every wave walks its tokens from zero; the waves then
 // share the chain of these ends, each taking some of the states, and walk again from their
 // starts with the outputs.
 // ---------------------------------------------------------------------------
 constexpr int kShort = 16;       // tokens of a wave
-constexpr int kShortCh = 16;     // channels of a workgroup
 
-template <typename T, int N, int kWaves>
+template <typename T, int N, int kWaves, int kLanes>
 __global__ __launch_bounds__(64 * kWaves) void scan_short_kernel(
     const T *__restrict__ x, const T *__restrict__ dt, const float *__restrict__ A,
     const T *__restrict__ B, const T *__restrict__ Cm, const float *__restrict__ D,
     const T *__restrict__ z, const float *__restrict__ dt_bias, const float *h0,
     const int32_t *__restrict__ lengths, T *__restrict__ y, float *hT, ScanDims m)
 {
-    constexpr int kOwn = N / 4;                          // states of a lane
+    constexpr int kCh = 64 / kLanes, kOwn = N / kLanes;  // channels of the workgroup, states of a lane
+    constexpr int kSide = 64 / kCh, kPass = kShort / kSide;   // tokens side by side, and passes over them
     constexpr int kRow = 2 * N, kQuads = kShort * kRow / 4, kPer = kQuads / 64;
     __shared__ __attribute__((aligned(16))) float bcs[kWaves][kShort * kRow];
-    __shared__ float2 dus[kWaves][kShort][kShortCh];     // step d, d x
-    __shared__ float ys[kWaves][kShort][kShortCh];
-    __shared__ float ends[kWaves][kOwn][64], sums[kWaves][kShortCh];
+    __shared__ float2 dus[kWaves][kShort][kCh];     // step d, d x
+    __shared__ float ys[kWaves][kShort][kCh];
+    __shared__ float ends[kWaves][kOwn][64], sums[kWaves][kCh];
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lane = threadIdx.x & 63;
-    const int tiles = (m.Cg + kShortCh - 1) / kShortCh;
+    const int tiles = (m.Cg + kCh - 1) / kCh;
     const int tile = blockIdx.x % tiles, g = blockIdx.x / tiles % m.G;
     const int64_t b = blockIdx.x / tiles / m.G;
-    const int first = g * m.Cg + tile * kShortCh, most = g * m.Cg + m.Cg - 1;
+    const int first = g * m.Cg + tile * kCh, most = g * m.Cg + m.Cg - 1;
     const int64_t len = tokens_of(lengths, b, m);
     const int t0 = wv * kShort;
     const int count = min(max((int)len - t0, 0), kShort);
     const int64_t row0 = b * m.L + t0;
 
-    // the walk's layout: channel lane / 4, states part * kOwn ...
-    const int ch = lane >> 2, part = lane & 3;
+    // the walk's layout: channel lane / kLanes, states part * kOwn ...
+    const int ch = lane / kLanes, part = lane % kLanes;
     const int c = min(first + ch, most);
     float a2[kOwn], h[kOwn];
 #pragma unroll
@@ -409,10 +409,11 @@ __global__ __launch_bounds__(64 * kWaves) void scan_short_kernel(
         a2[k] = kLog2e * A[(int64_t)c * N + part * kOwn + k];
         h[k] = 0.0f;
     }
-    // the inputs' layout: channel lane % 16, tokens lane / 16 + 4 j
-    const int ic = min(first + (lane & 15), most), it = lane >> 4;
-    const bool live = first + (lane & 15) <= most;
-    float xv[kShort / 4], zv[kShort / 4];
+    // the inputs' layout: channel lane % kCh, tokens lane / kCh + kSide j
+    const int il = lane % kCh, it = lane / kCh;
+    const int ic = min(first + il, most);
+    const bool live = first + il <= most;
+    float xv[kPass], zv[kPass];
     if (count > 0) {
         Quad<T> q[kPer];
 #pragma unroll
@@ -422,10 +423,10 @@ __global__ __launch_bounds__(64 * kWaves) void scan_short_kernel(
             const int n = i % (kRow / 4) * 4;
             q[j].load(n < N ? B + r * m.Bp + g * N + n : Cm + r * m.Cp + g * N + (n - N));
         }
-        float dv[kShort / 4];
+        float dv[kPass];
 #pragma unroll
-        for (int j = 0; j < kShort / 4; ++j) {
-            const int64_t r = row0 + min(it + 4 * j, count - 1);
+        for (int j = 0; j < kPass; ++j) {
+            const int64_t r = row0 + min(it + kSide * j, count - 1);
             xv[j] = (float)x[r * m.xp + ic];
             dv[j] = (float)dt[r * m.dtp + ic];
             zv[j] = z ? (float)z[r * m.zp + ic] : 0.0f;
@@ -435,10 +436,10 @@ __global__ __launch_bounds__(64 * kWaves) void scan_short_kernel(
         for (int j = 0; j < kPer; ++j)
             *reinterpret_cast<f32x4 *>(&bcs[wv][4 * (lane + 64 * j)]) = q[j].get();
 #pragma unroll
-        for (int j = 0; j < kShort / 4; ++j) {
+        for (int j = 0; j < kPass; ++j) {
             float d = dv[j] + bias;
             if (m.sp) d = softplus(d);
-            dus[wv][it + 4 * j][lane & 15] = make_float2(d, d * xv[j]);
+            dus[wv][it + kSide * j][il] = make_float2(d, d * xv[j]);
         }
     }
     auto states = [&](int i, int at, float *v) {         // kOwn values of B (at 0) or C (at N)
@@ -503,6 +504,7 @@ __global__ __launch_bounds__(64 * kWaves) void scan_short_kernel(
         }
         acc += dpp_move<0xb1, 0xf>(acc);     // quad_perm 1 0 3 2
         acc += dpp_move<0x4e, 0xf>(acc);     // quad_perm 2 3 0 1
+        if (kLanes == 8) acc += dpp_move<0x141, 0xf>(acc);     // row_half_mirror
         if (part == 0) ys[wv][i][ch] = acc;
     };
     // (four at a time by hand: the lane moves keep the compiler from it)
@@ -516,10 +518,10 @@ __global__ __launch_bounds__(64 * kWaves) void scan_short_kernel(
     for (; i0 < count; ++i0) token(i0);
     const float Dv = D ? D[ic] : 0.0f;
 #pragma unroll
-    for (int j = 0; j < kShort / 4; ++j) {
-        const int i = it + 4 * j;
+    for (int j = 0; j < kPass; ++j) {
+        const int i = it + kSide * j;
         if (i < count && live) {
-            float v = fmaf(Dv, xv[j], ys[wv][i][lane & 15]);
+            float v = fmaf(Dv, xv[j], ys[wv][i][il]);
             if (z) v *= silu(zv[j]);
             y[(row0 + i) * m.C + ic] = Elem<T>::from_f32(v);
         }
@@ -630,30 +632,45 @@ ScanDims dims_of(const ScanShape &s)
 
 int64_t waves_of(const ScanShape &s, const ScanDims &m) { return (int64_t)m.tiles * m.G * s.b; }
 
-// Waves of a workgroup where the scan runs as one launch, else 0: what one workgroup's LDS holds
-// (16 waves of 16 tokens, 8 for more than 32 states), up to 4096 waves.  One launch and segments,
-// in us: 64 tokens x 2048 channels x 16 states 7.5 and 12.4, 256 x 256 11.5 and 12.6, 128 x 512 x
-// 64 states 17.7 and 24.5; a single token 3.7 and (whole walks) 3.7, 16 tokens 5.5 and 8.0; at
-// 8192 waves (4 x 256 x 2048) 28.7 and 27.1.
-int short_waves(const ScanShape &s, int64_t N)
+// How a short scan is launched: waves of a workgroup (0: not as one launch), lanes of a channel.
+// One launch takes what a workgroup's LDS holds (16 waves of 16 tokens, 8 for more than 32
+// states), up to 4096 waves of four lanes a channel; eight lanes up to 2048 of these.  One launch
+// with eight lanes, with four, and segments, in us: 64 tokens x 2048 channels x 16 states 6.3,
+// 7.5 and 12.4, 256 x 256 8.5, 11.7 and 12.6, 100 x 512 x 64 states 11.2, 17.6 and 24; at 4096
+// waves (8 x 64 x 2048) 16.9, 12.5 and 21; at 8192 (4 x 256 x 2048) four lanes take 28.7,
+// segments 27.1.  A single token takes 3.3 against 3.7 for whole walks, 16 tokens 4.6 and 8.0.
+struct ShortPlan {
+    int waves, lanes;
+    int64_t groups;
+};
+ShortPlan short_plan(const ScanShape &s)
 {
-    constexpr int64_t kMost = 4096;
+    constexpr int64_t kMost = 4096, kEight = 2048;
     const int64_t waves = (s.L + kShort - 1) / kShort;
-    const int64_t groups = s.b * s.G * ((s.C / s.G + kShortCh - 1) / kShortCh);
-    return waves <= (N <= 32 ? 16 : 8) && waves * groups <= kMost ? (int)waves : 0;
+    const auto groups = [&](int64_t lanes) {
+        const int64_t ch = 64 / lanes;
+        return s.b * s.G * ((s.C / s.G + ch - 1) / ch);
+    };
+    ShortPlan p = {0, 4, groups(4)};
+    if (waves > (s.N <= 32 ? 16 : 8) || waves * p.groups > kMost) return p;
+    p.waves = (int)waves;
+    if (waves * p.groups <= kEight) p = {(int)waves, 8, groups(8)};
+    return p;
 }
 
 template <typename T, int N>
-hipError_t scan_short(const ScanShape &s, const ScanDims &m, const ScanArgs &a, hipStream_t st)
+hipError_t scan_short(const ShortPlan &p, const ScanDims &m, const ScanArgs &a, hipStream_t st)
 {
-    const int waves = short_waves(s, N);
-    const dim3 grid((unsigned)(s.b * s.G * ((m.Cg + kShortCh - 1) / kShortCh)));
-#define SSD_SHORT(W)                                                                              \
-    hipLaunchKernelGGL((scan_short_kernel<T, N, W>), grid, dim3(64 * waves), 0, st,               \
-                       (const T *)a.x, (const T *)a.dt, a.A, (const T *)a.B, (const T *)a.C, a.D, \
-                       (const T *)a.z, a.dt_bias, a.h0, a.lengths, (T *)a.y, a.hT, m)
-    if (waves <= 4) SSD_SHORT(4);
-    else SSD_SHORT((N <= 32 ? 16 : 8));
+#define SSD_SHORT(W, LANES)                                                                       \
+    hipLaunchKernelGGL((scan_short_kernel<T, N, W, LANES>), dim3((unsigned)p.groups),             \
+                       dim3(64 * p.waves), 0, st, (const T *)a.x, (const T *)a.dt, a.A,           \
+                       (const T *)a.B, (const T *)a.C, a.D, (const T *)a.z, a.dt_bias, a.h0,      \
+                       a.lengths, (T *)a.y, a.hT, m)
+    constexpr int kMost = N <= 32 ? 16 : 8;
+    if (p.lanes == 4 && p.waves <= 4) SSD_SHORT(4, 4);
+    else if (p.lanes == 4) SSD_SHORT(kMost, 4);
+    else if (p.waves <= 4) SSD_SHORT(4, 8);
+    else SSD_SHORT(kMost, 8);
 #undef SSD_SHORT
     return hipGetLastError();
 }
@@ -681,7 +698,8 @@ hipError_t scan_go(const ScanShape &s, const ScanArgs &a, float *h, hipStream_t 
                            a.D, (const T *)a.z, a.dt_bias, h, (T *)a.y, m, threads);
         return hipGetLastError();
     }
-    if (short_waves(s, N) > 0) return scan_short<T, N>(s, m, a, st);
+    const ShortPlan p = short_plan(s);
+    if (p.waves > 0) return scan_short<T, N>(p, m, a, st);
     const int64_t Cw = (int64_t)m.G * m.tiles * 64;
     ScanWs ws;
     ws.state = (float *)a.ws;
@@ -723,7 +741,7 @@ hipError_t scan_by_state(const ScanShape &s, const ScanArgs &a, float *h, hipStr
 size_t scan_workspace_bytes(const ScanShape &s)
 {
     const ScanDims m = dims_of(s);
-    if (m.S == 1 || short_waves(s, s.N) > 0) return SSD_SCAN_NO_WORKSPACE;
+    if (m.S == 1 || short_plan(s).waves > 0) return SSD_SCAN_NO_WORKSPACE;
     return (size_t)s.b * m.S * (s.N + 1) * m.G * m.tiles * 64 * sizeof(float);
 }
 

@@ -209,6 +209,19 @@ SCAN_CASES = [
     ("fp32", 2, 16, 17, 1, 16, dict(h0=False)),
     ("bf16", 1, 256, 50, 2, 16, {}),
     ("bf16", 1, 241, 31, 1, 32, dict(z=False, D=False)),
+    # short prompts of many channels: four lanes a channel, every state size
+    ("bf16", 20, 50, 520, 1, 8, {}),
+    ("fp32", 17, 33, 1030, 2, 16, {}),
+    ("bf16", 17, 34, 1001, 1, 24, {}),
+    ("bf16", 20, 49, 530, 1, 32, dict(h0=False)),
+    ("fp32", 20, 33, 600, 1, 40, {}),
+    ("bf16", 20, 40, 600, 1, 48, {}),
+    ("bf16", 20, 40, 600, 1, 56, {}),
+    ("fp32", 20, 35, 600, 1, 64, {}),
+    # ... and of few: eight lanes
+    ("bf16", 1, 33, 66, 1, 32, {}),
+    ("fp32", 1, 20, 30, 1, 40, {}),
+    ("bf16", 2, 128, 24, 1, 64, {}),
     # step sizes from e^-23 to 17: the far ends of the softplus
     ("fp32", 1, 200, 64, 1, 16, dict(spread=8.0)),
     ("bf16", 2, 90, 64, 1, 8, dict(spread=8.0)),
