@@ -14,9 +14,9 @@
 // steps is its decay), and one scans the segments again from there.  The first scan costs 0.8
 // of the second, and the bound is both.  Short prompts do the same within one workgroup and launch.
 //
-// Measured (bf16, 16384 tokens, 2048 channels, 16 states, gate and softplus): 207 us (100, 16
-// and 125 us for the two scans and the chain, each profiled by itself); the VALU slots of the two
-// scans are 223 us at the 2.04 GHz of an fma loop, HBM's floor is 53 us.  One whole walk per
+// Measured (bf16, 16384 tokens, 2048 channels, 16 states, gate and softplus): 204 to 209 us (96,
+// 128 and 16 us for the two scans and the chain, each profiled by itself); the VALU slots of the
+// two scans are 237 us at the 2.04 GHz of an fma loop, HBM's floor is 53 us.  One whole walk per
 // channel: 5.3 ms.
 
 #include <hip/hip_runtime.h>
