@@ -336,6 +336,17 @@ def test_scan_zero_state_under_growing_rates(L):
     ref.check(hT, rh, eh, "hT")
 
 
+def test_scan_many_segments():
+    """A long prompt of few channels: more segments than a chain workgroup holds at once."""
+    dev = require_gpu()
+    d = _scan_inputs("fp32", 1, 20011, 9, 1, 8, dev, 27, spread=0.5)
+    y, hT = _run_scan(d, True)
+    torch.cuda.synchronize()
+    ry, ey, rh, eh = _ref_scan(d, True)
+    ref.check(y, ry, ey, "y")
+    ref.check(hT, rh, eh, "hT")
+
+
 def test_scan_without_final_state():
     dev = require_gpu()
     for L in (1, 20, 200, 1300):
@@ -553,6 +564,83 @@ def test_given_stream_gets_its_own_memory():
         torch.cuda.synchronize()
         want = ssd.ssd_conv(conv[0], conv[1])[0], *_run_scan(d, True), ssd.ssd_norm(d["x"], w)
         assert all(torch.equal(p, q) for p, q in zip((u, y, hT, o), want))
+
+
+def test_two_streams_at_once():
+    """Calls in flight on two streams share nothing: the bits of calls in turn."""
+    dev = require_gpu()
+    cases = [(_scan_inputs("bf16", 1, 6000, 256, 1, 16, dev, 30 + i),
+              _conv_inputs("bf16", 1, 6000, 256, 4, dev, 32 + i)) for i in range(2)]
+    norm = (torch.ones(256, device=dev),)
+    want = [_block_calls(d, conv, norm, conv[3], d["h0"]) for d, conv in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(dev) for _ in cases]
+    for _ in range(3):
+        got = []
+        for s, (d, conv) in zip(streams, cases):
+            with torch.cuda.stream(s):
+                got.append(_block_calls(d, conv, norm, conv[3], d["h0"]))
+        torch.cuda.synchronize()
+        for p, q in zip(want, got):
+            assert all(torch.equal(a, b) for a, b in zip(p, q))
+
+
+def test_refusals():
+    """What a call cannot take raises, with nothing launched: the next call's outputs are right."""
+    dev = require_gpu()
+    bf, f32 = torch.bfloat16, torch.float32
+    z = lambda *s, dtype=bf: torch.zeros(*s, device=dev, dtype=dtype)
+    x, w = z(2, 5, 64), z(64, 4, dtype=f32)
+    for kw in (dict(weight=z(64, 4)), dict(weight=z(63, 4, dtype=f32)), dict(bias=z(64)),
+               dict(state=z(2, 2, 64)), dict(split=[32, 33]), dict(split=[64, 0]),
+               dict(split=[16] * 4), dict(lengths=torch.zeros(2, device=dev, dtype=torch.int64)),
+               dict(lengths=torch.zeros(2, dtype=torch.int32)), dict(y=z(2, 5, 32)),
+               dict(y=z(2, 64, 5).mT), dict(x=x.expand(3, 2, 5, 64)[0][:1].expand(2, 5, 64)),
+               dict(x=z(2, 5, 128)[:, :, ::2]), dict(x=z(2, 9, 64)[:, :5]), dict(x=x[0])):
+        with pytest.raises(ValueError):
+            ssd.ssd_conv(**{**dict(x=x, weight=w), **kw})
+    for k in (1, 5):
+        with pytest.raises(ssd.SsdError) as err:
+            ssd.ssd_conv(x, z(64, k, dtype=f32))
+        assert err.value.status == 3
+    with pytest.raises(ssd.SsdError) as err:      # weights that start off 16 bytes
+        ssd.ssd_conv(x, z(64 * 4 + 1, dtype=f32)[1:].view(64, 4))
+    assert err.value.status == 6
+
+    d = dict(x=x, dt=x, A=z(64, 16, dtype=f32), B=z(2, 5, 1, 16), C=z(2, 5, 1, 16))
+    for kw in (dict(A=z(64, 16)), dict(A=z(64, 8, dtype=f32)), dict(C=z(2, 5, 2, 16)), dict(dt=z(2, 5, 63)),
+               dict(h0=z(2, 64, 16)), dict(D=z(64)), dict(z=x.float()), dict(dt_bias=z(63, dtype=f32)),
+               dict(workspace=torch.zeros(1 << 20, dtype=torch.uint8)), dict(x=x[:, 0])):
+        with pytest.raises(ValueError):
+            ssd.ssd_scan(**{**d, **kw})
+    with pytest.raises(ssd.SsdError) as err:
+        ssd.ssd_scan(**{**d, "A": z(64, 12, dtype=f32), "B": z(2, 5, 1, 12), "C": z(2, 5, 1, 12)})
+    assert err.value.status == 3
+    with pytest.raises(ssd.SsdError) as err:      # bf16 rows of B that start off 4 bytes
+        ssd.ssd_scan(**{**d, "B": z(2, 5, 18)[:, :, 1:17].unflatten(2, (1, 16))})
+    assert err.value.status == 6
+    long = {k: (v if k == "A" else v.repeat_interleave(200, 1)) for k, v in d.items()}
+    with pytest.raises(ssd.SsdError) as err:
+        ssd.ssd_scan(**long, workspace=z(16, dtype=torch.uint8))
+    assert err.value.status == 4
+    with pytest.raises(ValueError):
+        ssd.ssd_scan_step(x[:, 0], x[:, 0], d["A"], d["B"][:, 0], d["C"][:, 0], None)
+    with pytest.raises(ValueError):
+        ssd.ssd_conv_step(x[:, 0], w, None, None)
+
+    for kw in (dict(weight=z(64)), dict(z=z(2, 5, 63)), dict(residual=z(2, 5, 64, dtype=torch.float16)),
+               dict(residual_out=z(2, 5, 64)), dict(y=x.float())):
+        with pytest.raises(ValueError):
+            ssd.ssd_norm(**{**dict(x=x, weight=z(64, dtype=f32)), **kw})
+    for kw in (dict(eps=0.0), dict(scale=float("inf")), dict(eps=float("nan"))):
+        with pytest.raises(ssd.SsdError) as err:
+            ssd.ssd_norm(x, z(64, dtype=f32), **kw)
+        assert err.value.status == 3
+    with pytest.raises(ssd.SsdError) as err:
+        ssd.ssd_norm(x, z(64, dtype=f32), ngroups=3)
+    assert err.value.status == 2
+    y = ssd.ssd_norm(torch.ones(1, 64, device=dev), torch.ones(64, device=dev))
+    assert abs(float(y[0, 0]) - 1) < 1e-4
 
 
 def test_step_plans_and_graph():
