@@ -52,6 +52,14 @@ __device__ __forceinline__ float softplus(float v)
     return fmaf(s, p, top);
 }
 
+// Orders LDS accesses of one wave's lanes for the compiler; the hardware carries a wave's LDS
+// accesses out in order, so no instruction is needed.
+__device__ __forceinline__ void wave_order()
+{
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
 struct ScanDims {
     int64_t L, xp, dtp, zp, Bp, Cp;
     int C, Cg, tiles;      // channels, channels per group, 64-channel tiles per group
@@ -234,13 +242,14 @@ __global__ __launch_bounds__(64) __attribute__((amdgpu_waves_per_eu(N <= 16 ? 4 
     };
     if (count > 0) fetch(0);
     for (int t = 0; t < count; t += kTile) {
-        // One wave: its LDS accesses are carried out in order, so the tile is written over the
-        // previous one's reads without a barrier.
+        // (one wave: the tile is written over the previous one's reads without a barrier)
+        wave_order();
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
             const int q = (int)threadIdx.x + 64 * j;
             if (kQuads % 64 == 0 || q < kQuads) *reinterpret_cast<f32x4 *>(bc + 4 * q) = bn[j].get();
         }
+        wave_order();
         float xv[kTile], dv[kTile], zv[kTile];
 #pragma unroll
         for (int i = 0; i < kTile; ++i) {
@@ -442,6 +451,7 @@ __global__ __launch_bounds__(64 * kWaves) void scan_short_kernel(
             dus[wv][it + kSide * j][il] = make_float2(d, d * xv[j]);
         }
     }
+    wave_order();
     auto states = [&](int i, int at, float *v) {         // kOwn values of B (at 0) or C (at N)
         const float *p = &bcs[wv][i * kRow + at + part * kOwn];
 #pragma unroll
@@ -516,6 +526,7 @@ __global__ __launch_bounds__(64 * kWaves) void scan_short_kernel(
         token(i0 + 3);
     }
     for (; i0 < count; ++i0) token(i0);
+    wave_order();
     const float Dv = D ? D[ic] : 0.0f;
 #pragma unroll
     for (int j = 0; j < kPass; ++j) {
