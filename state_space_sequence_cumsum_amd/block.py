@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 
 import torch
+from torch import Tensor
 
 from . import binding
 from .binding import SSD_BF16, SSD_F32, _raise
@@ -39,12 +40,15 @@ class NormProblem(ctypes.Structure):
 
 
 _lib = None
+_one_gpu = False     # set with _lib: a single GPU is always the current one
 
 
 def lib():
     """libssd.so with the argument types of this module's entry points."""
-    global _lib
+    global _lib, _one_gpu
     if _lib is None:
+        # (the count is final once the GPUs are in use)
+        _one_gpu = torch.cuda.is_initialized() and torch.cuda.device_count() == 1
         L = binding.lib()
         vp, st, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
         cp, sp, np_ = (ctypes.POINTER(t) for t in (ConvProblem, ScanProblem, NormProblem))
@@ -66,7 +70,7 @@ def lib():
 # (these run for every tensor of every call)
 # ---------------------------------------------------------------------------
 def _refuse(t, name, dtype, shape, device):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    if not isinstance(t, Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
     if device is not None and t.get_device() != device:
         raise ValueError(f"{name} is on {t.device}, expected cuda:{device}")
@@ -80,7 +84,7 @@ def _dense(t, name, dtype, shape, device):
     """The address of a contiguous tensor on GPU `device` (None for None)."""
     if t is None:
         return None
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+    if not (isinstance(t, Tensor) and t.dtype is dtype and t.shape == shape
             and t.get_device() == device and t.is_contiguous()):
         _refuse(t, name, dtype, shape, device)
         raise ValueError(f"{name} must be contiguous")
@@ -115,7 +119,7 @@ def _pitch(t, name, lead):
 
 def _rows(t, name, dtype, shape, device, lead):
     """(address, pitch) of a tensor on GPU `device` that _pitch takes."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+    if not (isinstance(t, Tensor) and t.dtype is dtype and t.shape == shape
             and t.get_device() == device):
         _refuse(t, name, dtype, shape, device)
     return t.data_ptr(), 0 if t.is_contiguous() else _pitch(t, name, lead)
@@ -123,7 +127,7 @@ def _rows(t, name, dtype, shape, device, lead):
 
 def _io(x, name="x"):
     """(dtype code, GPU index) of the tensor that sets both."""
-    code = _DTYPES.get(x.dtype) if isinstance(x, torch.Tensor) and x.is_cuda else None
+    code = _DTYPES.get(x.dtype) if isinstance(x, Tensor) and x.is_cuda else None
     if code is None:
         raise ValueError(f"{name} must be a float32 or bfloat16 GPU tensor")
     return code, x.get_device()
@@ -148,7 +152,7 @@ def _stream(stream, device):
 
 def _call(fn, args, device, what):
     """Calls a C entry point: kernels are launched for the tensors' GPU, whichever is current."""
-    if torch.cuda.current_device() == device:
+    if _one_gpu or torch.cuda.current_device() == device:
         st = fn(*args)
     else:
         with torch.cuda.device(device):
@@ -181,7 +185,7 @@ def _conv_args(x, weight, bias, state, silu, lengths, split, y, final_state, wan
     shape, td = x.shape, x.dtype
     if len(shape) != (2 if step else 3):
         raise ValueError(f"{what} takes x " + ("[b, channels]" if step else "[b, L, channels]"))
-    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+    if not isinstance(weight, Tensor) or weight.dim() != 2:
         raise ValueError("weight must be [channels, width]")
     b, c, k = shape[0], shape[-1], weight.shape[1]
     lead = tuple(shape[:-1])
@@ -197,7 +201,7 @@ def _conv_args(x, weight, bias, state, silu, lengths, split, y, final_state, wan
         ys = tuple([_empty((*lead, w), td, x.device, stream) for w in widths])
         yp = [t.data_ptr() for t in ys]
     else:
-        ys = (y,) if isinstance(y, torch.Tensor) else tuple(y)
+        ys = (y,) if isinstance(y, Tensor) else tuple(y)
         if len(ys) != n:
             raise ValueError(f"y must be {n} tensors, one per split width")
         yp = [_dense(t, "y", td, (*lead, w), dev) for t, w in zip(ys, widths)]
@@ -265,7 +269,7 @@ def _scan_inputs(x, dt, A, B, C, D, z, dt_bias, dt_softplus, lead):
     """(problem, GPU, addresses of x, dt, A, B, C, D, z, dt_bias)."""
     code, dev = _io(x)
     shape, td, f32 = x.shape, x.dtype, torch.float32
-    if not (isinstance(A, torch.Tensor) and isinstance(B, torch.Tensor) and len(shape) == lead + 1
+    if not (isinstance(A, Tensor) and isinstance(B, Tensor) and len(shape) == lead + 1
             and B.dim() == lead + 2 and A.dim() == 2):
         names = "[b, L, channels]" if lead == 2 else "[b, channels]"
         raise ValueError(f"the scan takes x {names}, B with [ngroups, dstate] in place of "
@@ -393,7 +397,7 @@ def ssd_norm(x, weight, z=None, residual=None, *, ngroups=1, eps=1e-5, scale=1.0
     rp = op = None
     rcode = SSD_F32
     if residual is not None:
-        rd = residual.dtype if isinstance(residual, torch.Tensor) else None
+        rd = residual.dtype if isinstance(residual, Tensor) else None
         if rd is not td and rd is not torch.float32:
             raise ValueError(f"residual has dtype {rd}, expected float32 or {td}")
         rcode = _DTYPES[rd]
