@@ -106,7 +106,7 @@ ssd::ScanShape scan_shape(const ssd_scan_problem *p)
     return s;
 }
 
-// B and C rows are read by scalar loads, which take whole dwords.
+// States and rates are read 16 bytes at a time; B and C four elements at a time, on 4 bytes.
 ssd_status check_scan_pointers(const ssd_scan_problem *p, const void *A, const void *B,
                                const void *C, std::initializer_list<const void *> states)
 {
