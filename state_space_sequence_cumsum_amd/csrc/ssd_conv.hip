@@ -12,7 +12,7 @@
 //
 // Measured (inputs not in the caches): 16384 x 2560 bf16, a slice of rows of 4640, 39 to 41 us
 // (4.2 TB/s; a 1 GiB copy reaches 5.1), 262144 x 1536 bf16 299 us (5.4 TB/s), 5 x 2500 x 777
-// bf16 one channel a thread 15.0 us (2.6 TB/s); 256 x 384 fp32 4.2 us, most of it the launch.
+// bf16 one channel a thread 14.0 us (2.8 TB/s); 256 x 384 fp32 4.2 us, most of it the launch.
 
 #include <hip/hip_runtime.h>
 
@@ -94,7 +94,14 @@ __global__ __launch_bounds__(kConvThreads) void conv_kernel(
     const T *state0, const int32_t *__restrict__ lengths, ConvOut<T> out, T *stateT, int L, int C,
     int64_t pitch, int groups, int tiles, int tt, int64_t threads, bool act)
 {
-    const int64_t id = (int64_t)blockIdx.x * kConvThreads + threadIdx.x;
+    // Rows off 16 bytes share cache lines with their neighbours: there an XCD (workgroups go to
+    // the eight in turn) takes one run of workgroups, so that its L2 completes these lines (5 x
+    // 2500 x 777 bf16 15.1 -> 14.0 us, 4000 x 1001 fp32 11.2 -> 10.6; 16384 x 2560 bf16 in whole
+    // lines 41.2 -> 42.0).
+    const unsigned run = gridDim.x / 8;
+    const unsigned block =
+        V == 1 && blockIdx.x < run * 8 ? blockIdx.x % 8 * run + blockIdx.x / 8 : blockIdx.x;
+    const int64_t id = (int64_t)block * kConvThreads + threadIdx.x;
     if (id >= threads) return;
     const int c = (int)(id % groups) * V;
     const int tile = (int)(id / groups % tiles);

@@ -137,6 +137,53 @@ def test_conv_step(dtype, b, split, k, cols, act, bias):
     assert torch.equal(state.cpu().double(), fin)
 
 
+@pytest.mark.parametrize("dtype,split,k,offset", [
+    ("bf16", [9, 8, 31], 3, 1), ("bf16", [777], 4, 3), ("bf16", [8, 17], 2, 0), ("bf16", [64, 7], 4, 5),
+    ("fp32", [5, 4, 7], 4, 1), ("fp32", [129], 2, 3), ("fp32", [64, 3], 3, 2)])
+def test_conv_outputs_and_states_off_16_bytes(dtype, split, k, offset):
+    """Outputs and states that start on any element, inside guarded buffers, the state in place:
+    the values are those of arrays of their own, and nothing next to them is written."""
+    dev = require_gpu()
+    b, L, c, lengths = 3, 43, sum(split), [43, 1, 20]
+    x, w, bv, s0 = _conv_inputs(dtype, b, L, c, k, dev, 31)
+    y, ey, fin = ref.conv(x, w, bv, s0, lengths, True)
+
+    def guarded(*shape):
+        n = 1
+        for m in shape:
+            n *= m
+        whole = torch.full((n + 24,), -7.0, device=dev, dtype=TD[dtype])
+        return whole, whole[offset:offset + n].view(shape)
+
+    def guards_hold(whole, view):
+        n = view.numel()
+        return bool((whole[:offset] == -7.0).all() and (whole[offset + n:] == -7.0).all())
+
+    outs = [guarded(b, L, m) for m in split]
+    whole_state, state = guarded(b, k - 1, c)
+    state.copy_(s0)
+    lt = torch.tensor(lengths, dtype=torch.int32, device=dev)
+    ssd.ssd_conv(x, w, bv, state, lengths=lt, split=split, y=[v for _, v in outs],
+                 final_state=state)
+    torch.cuda.synchronize()
+    got = torch.cat([v for _, v in outs], -1)
+    for i, n in enumerate(lengths):
+        ref.check(got[i, :n], y[i, :n], ey[i, :n], f"y of sequence {i}")
+        assert (got[i, n:] == -7.0).all()
+    assert torch.equal(state.cpu().double(), fin)
+    assert all(guards_hold(*o) for o in outs) and guards_hold(whole_state, state)
+
+    # the next token, from the same state
+    x1 = x[:, 7]
+    y, ey, fin = ref.conv(x1[:, None], w, bv, state.clone(), None, True)
+    outs = [guarded(b, m) for m in split]
+    ssd.ssd_conv_step(x1, w, bv, state, split=split, y=[v for _, v in outs])
+    torch.cuda.synchronize()
+    ref.check(torch.cat([v for _, v in outs], -1), y[:, 0], ey[:, 0], "y of a step")
+    assert torch.equal(state.cpu().double(), fin)
+    assert all(guards_hold(*o) for o in outs) and guards_hold(whole_state, state)
+
+
 def test_conv_lengths_out_of_range_are_clamped():
     """Lengths are data on the device: below 0 counts as 0, above L as L."""
     dev = require_gpu()
