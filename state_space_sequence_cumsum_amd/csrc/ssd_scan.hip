@@ -172,31 +172,6 @@ __global__ __launch_bounds__(64) __attribute__((amdgpu_waves_per_eu(N <= 16 ? 4 
     const int64_t slot = b * m.S + seg;
     const int cw = wave * 64 + threadIdx.x;
 
-    float a2[N], h[N];
-#pragma unroll
-    for (int n = 0; n < N; n += 4) {
-        const f32x4 v = *reinterpret_cast<const f32x4 *>(A + (int64_t)c * N + n);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) a2[n + i] = kLog2e * v[i];
-    }
-#pragma unroll
-    for (int n = 0; n < N; ++n) h[n] = 0.0f;
-    if (KIND == kWhole && h0) {
-#pragma unroll
-        for (int n = 0; n < N; n += 4) {
-            const f32x4 v = *reinterpret_cast<const f32x4 *>(h0 + (b * m.C + c) * N + n);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) h[n + i] = v[i];
-        }
-    }
-    if (KIND == kOut) {
-#pragma unroll
-        for (int n = 0; n < N; ++n) h[n] = ws.state[(slot * N + n) * Cw + cw];
-    }
-    const float bias = dt_bias ? dt_bias[c] : 0.0f;
-    const float Dv = KIND != kEnds && D ? D[c] : 0.0f;
-    float steps = 0.0f;
-
     // A tile's rows are buffers that start at its first token's row; lane offset + row offset
     // stay far below kRange (at most kTile rows of 2^24 elements).  Lanes past the group's end
     // have an offset at its end: they read zeros and store nothing.
@@ -240,7 +215,34 @@ __global__ __launch_bounds__(64) __attribute__((amdgpu_waves_per_eu(N <= 16 ? 4 
             if (KIND != kEnds) zn[i] = buf_load<T>(zs, lane_off, r * zp);
         }
     };
+    // the first tile before the rates and states, so that these arrive with it (1024 tokens of
+    // 2048 channels 27.6 -> 27.0 us)
     if (count > 0) fetch(0);
+    float a2[N], h[N];
+#pragma unroll
+    for (int n = 0; n < N; n += 4) {
+        const f32x4 v = *reinterpret_cast<const f32x4 *>(A + (int64_t)c * N + n);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a2[n + i] = kLog2e * v[i];
+    }
+#pragma unroll
+    for (int n = 0; n < N; ++n) h[n] = 0.0f;
+    if (KIND == kWhole && h0) {
+#pragma unroll
+        for (int n = 0; n < N; n += 4) {
+            const f32x4 v = *reinterpret_cast<const f32x4 *>(h0 + (b * m.C + c) * N + n);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) h[n + i] = v[i];
+        }
+    }
+    if (KIND == kOut) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) h[n] = ws.state[(slot * N + n) * Cw + cw];
+    }
+    const float bias = dt_bias ? dt_bias[c] : 0.0f;
+    const float Dv = KIND != kEnds && D ? D[c] : 0.0f;
+    float steps = 0.0f;
+
     for (int t = 0; t < count; t += kTile) {
         // (one wave: the tile is written over the previous one's reads without a barrier)
         wave_order();
@@ -328,7 +330,8 @@ __global__ __launch_bounds__(64 * kRunWaves) void scan_chain_kernel(
     const int in_group = (wave % m.tiles) * 64 + lane;
     const bool live = in_group < m.Cg;
     const int c = wave / m.tiles * m.Cg + min(in_group, m.Cg - 1);
-    const float a2 = kLog2e * A[(int64_t)c * N + n];
+    // (scaled at its use: the loads below are not to wait for it)
+    const float rate = A[(int64_t)c * N + n];
     float h = h0 && live ? h0[(b * m.C + c) * N + n] : 0.0f;
     float *st = ws.state + (b * m.S * N + n) * Cw + wave * 64;
     const float *sm = ws.steps + b * m.S * Cw + wave * 64;
@@ -351,7 +354,7 @@ __global__ __launch_bounds__(64 * kRunWaves) void scan_chain_kernel(
 #pragma unroll
         for (int i = 0; i < kRun; ++i) {
             if (i < ends) {
-                d[i] = finite_exp2(a2 * d[i]);
+                d[i] = finite_exp2(rate * (kLog2e * d[i]));
                 end = fmaf(d[i], end, e[i]);
                 decay = fminf(decay * d[i], 3.4028235e38f);
             }
