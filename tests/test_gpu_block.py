@@ -318,6 +318,34 @@ def test_scan_ragged(dtype, L, c, G, N, lengths):
     ref.check(hT, rh, eh, "hT")
 
 
+@pytest.mark.parametrize("dtype,b,c,G,N", [
+    ("bf16", 1024, 9, 1, 8), ("fp32", 512, 66, 1, 16), ("bf16", 512, 6, 2, 24),
+    ("fp32", 1030, 5, 1, 32), ("bf16", 1024, 4, 1, 40), ("fp32", 1024, 3, 1, 48),
+    ("bf16", 512, 4, 2, 56), ("fp32", 1024, 2, 1, 64), ("bf16", 1024, 3, 1, 64)])
+def test_scan_ragged_batch_of_whole_walks(dtype, b, c, G, N):
+    """A wave for each of 1024 sequences or more, with every length from none to all tokens."""
+    dev = require_gpu()
+    L = 70
+    lengths = [(i * 37) % (L + 1) for i in range(b)]
+    d = _scan_inputs(dtype, b, L, c, G, N, dev, 41)
+    past = torch.arange(L)[None, :] >= torch.tensor(lengths)[:, None]
+    past = past.to(dev)
+    clean = {k: None if v is None else v.clone() for k, v in d.items()}
+    for k in ("x", "dt", "B", "C", "z"):
+        d[k][past] = float("nan")
+        clean[k][past] = 0
+    y = torch.full((b, L, c), -7.0, device=dev, dtype=TD[dtype])
+    _, hT = _run_scan(d, True, y=y, lengths=torch.tensor(lengths, dtype=torch.int32, device=dev))
+    torch.cuda.synchronize()
+    ry, ey, rh, eh = _ref_scan(clean, True, lengths)
+    assert (y[past] == -7.0).all(), "rows behind a sequence were written"
+    live = ~past.cpu()
+    ref.check(y.cpu()[live], ry[live], ey[live], "y")
+    ref.check(hT, rh, eh, "hT")
+    empty = [i for i, n in enumerate(lengths) if n == 0]
+    assert torch.equal(hT[empty], d["h0"][empty])
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_scan_column_slices(dtype):
     """Inputs that are columns of wider arrays give the bits of dense ones."""
