@@ -228,7 +228,8 @@ template <typename T, typename R, int V> hipError_t norm_team(NormArgs<T, R> a, 
     }
     if (vectors <= 64 * kWave / 2) return norm_go<T, R, V, kWave / 2, false>(a, st);
     if (vectors <= 64 * kWave) return norm_go<T, R, V, kWave, false>(a, st);
-    if (vectors <= kNormThreads * kGroup / 4) return norm_go<T, R, V, kGroup / 4, true>(a, st);
+    if constexpr (kGroup / 4 * kNormThreads > 64 * kWave)     // (single elements: a wave's reach)
+        if (vectors <= kNormThreads * kGroup / 4) return norm_go<T, R, V, kGroup / 4, true>(a, st);
     if (vectors <= kNormThreads * kGroup / 2) return norm_go<T, R, V, kGroup / 2, true>(a, st);
     if (vectors <= kNormThreads * kGroup) return norm_go<T, R, V, kGroup, true>(a, st);
     hipLaunchKernelGGL((norm_long_kernel<T, R, V>), dim3((unsigned)a.items), dim3(kNormThreads), 0,

@@ -492,6 +492,11 @@ NORM_CASES = [
     ("bf16", 2100, 4096, 1, "none", "bf16", (0, 0)),
     ("fp32", 70003, 32, 1, "after", None, (0, 0)),
     ("bf16", 4001, 1032, 3, "first", "fp32", (0, 8)),
+    # single elements in a wave, and in a workgroup
+    ("bf16", 5, 999, 1, "after", "bf16", (0, 0)),
+    ("fp32", 3, 1501, 1, "first", "fp32", (0, 0)),
+    ("bf16", 4, 2049, 1, "none", "fp32", (0, 0)),
+    ("bf16", 2300, 4095, 1, "first", None, (1, 0)),
 ]
 
 
