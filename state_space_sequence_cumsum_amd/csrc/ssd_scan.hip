@@ -11,7 +11,7 @@
 // output), which bound the scan before HBM does.  Where the channels give too few waves, the
 // tokens are split into segments: one launch scans each segment from zero for its end state, a
 // short one chains these into the segments' start states (exp of A times a segment's summed
-// steps is its decay), and one scans the segments again from there.  The first scan costs 0.8
+// steps is its factor), and one scans the segments again from there.  The first scan costs 0.8
 // of the second, and the bound is both.  Short prompts do the same within one workgroup and launch.
 //
 // Measured (bf16, 16384 tokens, 2048 channels, 16 states, gate and softplus): 204 to 209 us (96,
@@ -305,9 +305,27 @@ __global__ __launch_bounds__(64) __attribute__((amdgpu_waves_per_eu(N <= 16 ? 4 
     }
 }
 
-// exp2(v), finite: under positive rates a segment's decay may overflow where token by token
-// nothing would, and a state that is still zero has to stay zero under it.
-__device__ __forceinline__ float finite_exp2(float v) { return fminf(fast_exp2(v), 3.4028235e38f); }
+// The factor 2^v of a whole segment, as f 2^k with f in [0.7, 1.42]: with growing states, or
+// quickly shrinking ones, it may leave fp32's range where the states on both sides of it do not,
+// and a state that is still zero has to stay zero under it.  Past +-600 every state but zero and
+// infinity becomes infinite or zero (2^-149 to 2^128 are 277 apart); a NaN among the steps or
+// rates is in the segment's end state too.
+struct Factor {
+    float f;
+    int k;
+    __device__ __forceinline__ void set(float v)
+    {
+        v = __builtin_amdgcn_fmed3f(v, -600.0f, 600.0f);
+        const float whole = __builtin_rintf(v);
+        f = fast_exp2(v - whole);
+        k = (int)whole;
+    }
+    // 2^v h + end
+    __device__ __forceinline__ float apply(float h, float end) const
+    {
+        return fmaf(f, __builtin_ldexpf(h, k), end);
+    }
+};
 
 // Turns the segments' end states (each from zero) into their start states, in place: along
 // the segments, start[0] = h0 and start[s + 1] = exp(A sum of steps of s) start[s] + end[s].
@@ -320,7 +338,8 @@ __global__ __launch_bounds__(64 * kRunWaves) void scan_chain_kernel(
     const float *__restrict__ A, const float *h0, const int32_t *__restrict__ lengths, ScanWs ws,
     int N, ScanDims m)
 {
-    __shared__ float run_decay[kRunWaves][64], run_end[kRunWaves][64];
+    __shared__ Factor run_factor[kRunWaves][64];
+    __shared__ float run_end[kRunWaves][64];
     const uint32_t lane = threadIdx.x & 63;
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int gt = m.G * m.tiles;
@@ -343,6 +362,7 @@ __global__ __launch_bounds__(64 * kRunWaves) void scan_chain_kernel(
         const int first = s0 + wv * per;
         const int starts = min(per, S - first), ends = min(per, S - 1 - first);
         float e[kRun], d[kRun];
+        Factor step[kRun];
 #pragma unroll
         for (int i = 0; i < kRun; ++i) {
             if (i < ends) {
@@ -350,28 +370,30 @@ __global__ __launch_bounds__(64 * kRunWaves) void scan_chain_kernel(
                 d[i] = (sm + (first + i) * Cw)[lane];
             }
         }
-        float decay = 1.0f, end = 0.0f;
+        // a run's factor by its exponent, the sum of the segments'
+        float log_sum = 0.0f, end = 0.0f;
 #pragma unroll
         for (int i = 0; i < kRun; ++i) {
             if (i < ends) {
-                d[i] = finite_exp2(rate * (kLog2e * d[i]));
-                end = fmaf(d[i], end, e[i]);
-                decay = fminf(decay * d[i], 3.4028235e38f);
+                const float v = rate * (kLog2e * d[i]);
+                step[i].set(v);
+                end = step[i].apply(end, e[i]);
+                log_sum += v;
             }
         }
-        run_decay[wv][lane] = decay;
+        run_factor[wv][lane].set(log_sum);
         run_end[wv][lane] = end;
         __syncthreads();
         float mine = h;
         for (int w = 0; w < nw; ++w) {
             if (w == wv) mine = h;
-            h = fmaf(run_decay[w][lane], h, run_end[w][lane]);
+            h = run_factor[w][lane].apply(h, run_end[w][lane]);
         }
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < kRun; ++i) {
             if (i < starts) (st + (int64_t)(first + i) * N * Cw)[lane] = mine;
-            if (i < ends) mine = fmaf(d[i], mine, e[i]);
+            if (i < ends) mine = step[i].apply(mine, e[i]);
         }
     }
 }
@@ -485,19 +507,20 @@ __global__ __launch_bounds__(64 * kWaves) void scan_short_kernel(
         for (int k = wv; k < kOwn; k += nw) {
             const float rate = kLog2e * A[(int64_t)c * N + part * kOwn + k];
             float now = h0 ? h0[(b * m.C + c) * N + part * kOwn + k] : 0.0f;
-            float e[kWaves], d[kWaves];
+            float e[kWaves];
+            Factor step[kWaves];
 #pragma unroll
             for (int w = 0; w < kWaves; ++w) {
                 if (w < nw) {
                     e[w] = ends[w][k][lane];
-                    d[w] = finite_exp2(rate * sums[w][ch]);
+                    step[w].set(rate * sums[w][ch]);
                 }
             }
 #pragma unroll
             for (int w = 0; w < kWaves; ++w) {
                 if (w < nw) {
                     ends[w][k][lane] = now;
-                    now = fmaf(d[w], now, e[w]);
+                    now = step[w].apply(now, e[w]);
                 }
             }
         }

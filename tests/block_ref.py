@@ -70,8 +70,9 @@ def conv(x, weight, bias, state, lengths, act):
     return y, ey, final
 
 
-def scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, lengths=None, act=False):
-    """x, dt, z [b, L, c]; B, C [b, L, G, N] -> (y, bound, hT, bound).
+def scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, lengths=None, act=False, run=None):
+    """x, dt, z [b, L, c]; B, C [b, L, G, N] -> (y, bound, hT, bound).  run: the most roundings
+    that a sum of steps goes through where tokens are split into runs (None: L).
 
     Negative step sizes grow a state exponentially.  Once the magnitude of a state, or of the
     terms of an output, passes 2^127, fp32 cannot hold it (its largest value is 2^128 - 2^104):
@@ -101,8 +102,8 @@ def scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, lengths=None, ac
         a = torch.exp(dv * A)
         # the exponent: A log2(e) and its product with d rounded (3 U with the constant), d
         # itself off by ed; where tokens are split into runs, exp of a run's summed steps
-        # carries the sum's error, at most L U of it, in place of the single steps'
-        ea = rate * (3 + L) * U + ed[:, t, :, None] * A.abs() + 2 * U
+        # carries the sum's error, at most L (or run) U of it, in place of the single steps'
+        ea = rate * (3 + (L if run is None else run)) * U + ed[:, t, :, None] * A.abs() + 2 * U
         term = dv * xv * B[:, t]
         et = term.abs() * 2 * U + ed[:, t, :, None] * (xv * B[:, t]).abs()
         new = a * h + term
