@@ -307,7 +307,8 @@ ssd_status ssd_workspace_layout(const ssd_problem *problem, size_t *off_G2, size
  *     tokens of each sequence of a padded batch, each taken as at least 0 and at most
  *     seqlen.  Rows behind a sequence's length are not read and their outputs are left as
  *     they were; the final state is the one after the sequence's own last token (with
- *     length 0 the initial state, or zeros).
+ *     length 0 the initial state, or zeros).  ssd_forward has no lengths: what goes on into it
+ *     (x, B, C, and dt) has to be zero behind a sequence, where a token then changes nothing.
  *   - element alignment is enough for x, z, dt, y, the conv states and the residual
  *     stream (rows on 16 bytes run faster); stricter cases are named per entry point.
  *   - exponentials, sums, states and norms are fp32; each output is rounded once.

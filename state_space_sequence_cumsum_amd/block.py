@@ -3,8 +3,8 @@
 Argument marshalling only, as in :mod:`.binding`: every function checks placement, dtype,
 shape and layout of its tensors and calls the C entry point of the same name on the current
 (or given) HIP stream.  Inputs may be column slices of a wider projection output (rows dense,
-one pitch from token to token); outputs and states are contiguous and allocated with
-``torch.empty`` when not given.  Forward only: none of these functions records a gradient.
+one pitch from token to token); outputs and states are contiguous and allocated when not given
+(with ``torch.empty``, or as zeros where ``lengths`` leave rows of them unwritten).  Forward only: none of these functions records a gradient.
 """
 from __future__ import annotations
 
@@ -133,15 +133,28 @@ def _io(x, name="x"):
     return code, x.get_device()
 
 
-def _empty(shape, dtype, device, stream):
+def _empty(shape, dtype, device, stream, make=torch.empty):
     """A new tensor for a call on `stream` (None: the current one): it comes from that stream's
     memory, which earlier work on the current stream may not be using any more."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return make(shape, dtype=dtype, device=device)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return make(shape, dtype=dtype, device=device)
+
+
+def _cleared(lead, widths, dtype, device, stream):
+    """New tensors [*lead, width] of zeros, for outputs whose rows behind a sequence's length the
+    kernels leave as they are: parts of one buffer, each on 256 bytes, cleared by one launch."""
+    if len(widths) == 1:
+        return (_empty((*lead, widths[0]), dtype, device, stream, torch.zeros),)
+    rows = lead[0] * lead[1]
+    starts = [0]
+    for w in widths:
+        starts.append(starts[-1] + (rows * w + 127) // 128 * 128)
+    whole = _empty((starts[-1],), dtype, device, stream, torch.zeros)
+    return tuple([whole[at:at + rows * w].view(*lead, w) for at, w in zip(starts, widths)])
 
 
 def _stream(stream, device):
@@ -198,7 +211,10 @@ def _conv_args(x, weight, bias, state, silu, lengths, split, y, final_state, wan
     bp = _dense(bias, "bias", torch.float32, (c,), dev)
     sp = _dense(state, "state", td, (b, k - 1, c), dev)
     if y is None:
-        ys = tuple([_empty((*lead, w), td, x.device, stream) for w in widths])
+        if lengths is None:
+            ys = tuple([_empty((*lead, w), td, x.device, stream) for w in widths])
+        else:
+            ys = _cleared(lead, widths, td, x.device, stream)
         yp = [t.data_ptr() for t in ys]
     else:
         ys = (y,) if isinstance(y, Tensor) else tuple(y)
@@ -233,8 +249,9 @@ def ssd_conv(x, weight, bias=None, state=None, *, silu=True, lengths=None, split
     with 2 to 4 taps and bias [channels], float32; state [b, width-1, channels] the inputs
     before the first token (None: zeros).  ``split``: up to three widths with sum channels,
     the output then comes as that many contiguous tensors (x, B and C of ssd_forward).
-    ``lengths`` [b] int32: tokens of each sequence; rows of y behind them are left as they
-    were.  ``final_state`` may be ``state`` itself.  Returns (y or a tuple of them, final
+    ``lengths`` [b] int32: tokens of each sequence; rows behind them are left as they were in a
+    given y, and zeros in one allocated here (ssd_forward, which has no lengths, then takes x, B
+    and C with a dt of zero behind them).  ``final_state`` may be ``state`` itself.  Returns (y or a tuple of them, final
     state or None)."""
     args, dev, out, final, _ = _conv_args(x, weight, bias, state, silu, lengths, split, y,
                                           final_state, want_final, stream, False)
@@ -307,8 +324,8 @@ def ssd_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, *, dt_softpl
     x, dt and z (the gate, optional) [b, L, channels]; B, C [b, L, ngroups, dstate]; A
     [channels, dstate], D and dt_bias [channels] (optional) and h0 [b, channels, dstate]
     (None: zeros) float32.  ``dt_softplus``: the step size is log(1 + exp(dt + dt_bias)).
-    ``lengths`` [b] int32: tokens of each sequence; rows of y behind them are left as they
-    were and hT is the state after each sequence's own last token.  hT may be h0 itself.
+    ``lengths`` [b] int32: tokens of each sequence; rows behind them are left as they were in a
+    given y and zeros in one allocated here, and hT is the state after each sequence's own last token.  hT may be h0 itself.
     Returns (y [b, L, channels], hT [b, channels, dstate] float32 or None)."""
     prob, dev, ptrs = _scan_inputs(x, dt, A, B, C, D, z, dt_bias, dt_softplus, 2)
     td, f32 = x.dtype, torch.float32
@@ -316,7 +333,7 @@ def ssd_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, *, dt_softpl
     hp = _dense(h0, "h0", f32, states, dev)
     lp = _dense(lengths, "lengths", torch.int32, (prob.batch,), dev)
     if y is None:
-        y = _empty(x.shape, td, x.device, stream)
+        y = _empty(x.shape, td, x.device, stream, torch.empty if lengths is None else torch.zeros)
         yp = y.data_ptr()
     else:
         yp = _dense(y, "y", td, x.shape, dev)
