@@ -78,7 +78,9 @@ typedef enum {
     SSD_ERR_MISALIGNED = 6,   /* a vector-accessed array does not start on 16 bytes  */
     SSD_ERR_SCRATCH = 7,      /* ssd_forward_noalloc: the problem needs more than
                                  SSD_SCRATCH_BYTES of workspace                         */
-    SSD_ERR_PLAN = 8          /* a launch plan the kernels cannot run for the problem   */
+    SSD_ERR_PLAN = 8,         /* a launch plan the kernels cannot run for the problem   */
+    SSD_ERR_OVERLAP = 9       /* an output shares memory with another argument (checked by
+                                 the operators around the forward)                      */
 } ssd_status;
 
 typedef enum { SSD_F32 = 0, SSD_BF16 = 1 } ssd_dtype;
@@ -312,6 +314,10 @@ ssd_status ssd_workspace_layout(const ssd_problem *problem, size_t *off_G2, size
  *   - element alignment is enough for x, z, dt, y, the conv states and the residual
  *     stream (rows on 16 bytes run faster); stricter cases are named per entry point.
  *   - exponentials, sums, states and norms are fp32; each output is rounded once.
+ *   - an output that shares memory with another argument returns SSD_ERR_OVERLAP, but for
+ *     a final state in its initial state's buffer, and, in ssd_norm and the single-token
+ *     entry points, an output in the buffer of an input with its rows, type and dense
+ *     layout (x and z, dt, the residual stream).
  * ------------------------------------------------------------------------- */
 
 /* Short causal depthwise convolution.  For every channel c, with K = width taps,

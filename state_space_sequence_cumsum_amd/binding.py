@@ -23,7 +23,7 @@ SSD_F32, SSD_BF16 = 0, 1
 FORWARD_EVENTS = 5      # SSD_FORWARD_EVENTS: marks around stage 1, state pass, group scan, stage 3
 STATUS = {0: "SSD_OK", 1: "SSD_ERR_NULL_ARG", 2: "SSD_ERR_BAD_SHAPE", 3: "SSD_ERR_UNSUPPORTED",
           4: "SSD_ERR_WORKSPACE", 5: "SSD_ERR_HIP", 6: "SSD_ERR_MISALIGNED", 7: "SSD_ERR_SCRATCH",
-          8: "SSD_ERR_PLAN"}
+          8: "SSD_ERR_PLAN", 9: "SSD_ERR_OVERLAP"}
 SCRATCH_BYTES = 128 << 20   # SSD_SCRATCH_BYTES: the static workspace of ssd_forward_noalloc
 
 

@@ -4,7 +4,10 @@ Argument marshalling only, as in :mod:`.binding`: every function checks placemen
 shape and layout of its tensors and calls the C entry point of the same name on the current
 (or given) HIP stream.  Inputs may be column slices of a wider projection output (rows dense,
 one pitch from token to token); outputs and states are contiguous and allocated when not given
-(with ``torch.empty``, or as zeros where ``lengths`` leave rows of them unwritten).  Forward only: none of these functions records a gradient.
+(with ``torch.empty``, or as zeros where ``lengths`` leave rows of them unwritten).  An output
+may be a final state in its initial state's tensor, and in the step functions and the norm an
+input of its own dense layout; otherwise one that shares memory with another argument is
+refused.  Forward only: none of these functions records a gradient.
 """
 from __future__ import annotations
 

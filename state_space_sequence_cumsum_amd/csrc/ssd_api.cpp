@@ -406,6 +406,7 @@ const char *ssd_status_string(ssd_status status)
         return "the problem needs more workspace than the static scratch of ssd_forward_noalloc "
                "holds (SSD_SCRATCH_BYTES); use ssd_forward with a workspace";
     case SSD_ERR_PLAN: return "the launch plan is not one the kernels can run for this problem";
+    case SSD_ERR_OVERLAP: return "an output shares memory with another argument";
     }
     return "unknown status";
 }

@@ -133,6 +133,98 @@ ssd_status check_norm(const ssd_norm_problem *p)
     return SSD_OK;
 }
 
+// ---------------------------------------------------------------------------
+// Outputs and inputs apart.  The kernels read inputs that other threads' outputs would have
+// replaced (a token tile of the convolution reads the rows before it), so memory that an output
+// shares with another argument is refused.  `rows` rows of `width` bytes, `pitch` bytes apart;
+// `same`: an output with this very layout may be this buffer (each element is read before the
+// same thread writes it).
+// ---------------------------------------------------------------------------
+struct Area {
+    const void *p;
+    int64_t rows, pitch, width;
+    bool same;
+};
+
+int64_t bytes_of(int32_t dtype) { return dtype == SSD_BF16 ? 2 : 4; }
+
+Area dense(const void *p, int64_t bytes, bool same = false) { return {p, 1, bytes, bytes, same}; }
+
+// rows of `width` elements at a pitch of `pitch` elements (0: dense)
+Area rows_of(const void *p, int64_t rows, int64_t pitch, int64_t width, int64_t bytes,
+             bool same = false)
+{
+    if (pitch == 0 || pitch == width || rows == 1) return dense(p, rows * width * bytes, same);
+    return {p, rows, pitch * bytes, width * bytes, same};
+}
+
+// Whether a dense output shares memory with `in`.
+bool meet(const Area &out, const Area &in)
+{
+    if (out.p == nullptr || in.p == nullptr) return false;
+    // the output's start from the input's, and the input's first row that ends behind it
+    const int64_t d = (int64_t)(reinterpret_cast<uintptr_t>(out.p) - reinterpret_cast<uintptr_t>(in.p));
+    const int64_t row = d < in.width ? 0 : (d - in.width) / in.pitch + 1;
+    if (row >= in.rows || row * in.pitch >= d + out.width) return false;
+    return !(in.same && d == 0 && in.rows == 1 && in.width == out.width);
+}
+
+ssd_status check_apart(std::initializer_list<Area> outs, std::initializer_list<Area> ins)
+{
+    for (const Area *o = outs.begin(); o != outs.end(); ++o) {
+        for (const Area &in : ins)
+            if (meet(*o, in)) return SSD_ERR_OVERLAP;
+        for (const Area *p = o + 1; p != outs.end(); ++p)
+            if (meet(*o, *p)) return SSD_ERR_OVERLAP;
+    }
+    return SSD_OK;
+}
+
+// The convolution's arrays; the final state may be the state's buffer, and a step's only output
+// may be x.
+ssd_status check_conv_areas(const ssd_conv_problem *p, const void *x, const float *weight,
+                            const float *bias, const void *state0, const int32_t *lengths,
+                            const void *y0, const void *y1, const void *y2, const void *stateT,
+                            bool step)
+{
+    const int64_t e = bytes_of(p->dtype), rows = p->batch * p->seqlen, C = p->channels;
+    const int64_t state = p->batch * (p->width - 1) * C * e;
+    const ssd_status st =
+        check_apart({dense(y0, rows * p->split[0] * e), dense(y1, rows * p->split[1] * e),
+                     dense(y2, rows * p->split[2] * e)},
+                    {rows_of(x, rows, p->x_pitch, C, e, step), dense(weight, C * p->width * 4),
+                     dense(bias, C * 4), dense(state0, state), dense(lengths, p->batch * 4),
+                     dense(stateT, state)});
+    if (st != SSD_OK) return st;
+    return check_apart({dense(stateT, state)},
+                       {rows_of(x, rows, p->x_pitch, C, e), dense(weight, C * p->width * 4),
+                        dense(bias, C * 4), dense(state0, state, true),
+                        dense(lengths, p->batch * 4)});
+}
+
+// The scan's arrays: hT may be h0's buffer, and a step's y the buffer of x, dt or z.
+ssd_status check_scan_areas(const ssd_scan_problem *p, const ssd::ScanArgs &a, const void *hT,
+                            size_t workspace_bytes, bool step)
+{
+    const int64_t e = bytes_of(p->dtype), rows = p->batch * p->seqlen, C = p->channels;
+    const int64_t gn = p->ngroups * p->dstate, state = p->batch * C * p->dstate * 4;
+    const Area y = dense(a.y, rows * C * e), h = dense(hT, state);
+    const Area ws = dense(workspace_bytes ? a.ws : nullptr, (int64_t)workspace_bytes);
+    const Area A = dense(a.A, C * p->dstate * 4), D = dense(a.D, C * 4),
+               bias = dense(a.dt_bias, C * 4), lengths = dense(a.lengths, p->batch * 4),
+               B = rows_of(a.B, rows, p->B_pitch, gn, e), Cm = rows_of(a.C, rows, p->C_pitch, gn, e);
+    const auto row = [&](const void *q, int64_t pitch, bool same) {
+        return rows_of(q, rows, pitch, C, e, same);
+    };
+    const ssd_status st = check_apart(
+        {y}, {row(a.x, p->x_pitch, step), row(a.dt, p->dt_pitch, step), row(a.z, p->z_pitch, step),
+              A, B, Cm, D, bias, lengths, dense(a.h0, state), h, ws});
+    if (st != SSD_OK) return st;
+    return check_apart({h, ws}, {row(a.x, p->x_pitch, false), row(a.dt, p->dt_pitch, false),
+                                 row(a.z, p->z_pitch, false), A, B, Cm, D, bias, lengths,
+                                 dense(a.h0, state, true)});
+}
+
 ssd_status status_of(hipError_t e) { return ssd_status(ssd::hip_status(e)); }
 
 }  // namespace
@@ -150,6 +242,10 @@ ssd_status ssd_conv(const ssd_conv_problem *problem, const void *x, const float 
     if (!x || !weight || !y0 || (problem->split[1] > 0 && !y1) || (problem->split[2] > 0 && !y2))
         return SSD_ERR_NULL_ARG;
     if (!on_bytes(16, {weight, bias})) return SSD_ERR_MISALIGNED;
+    const ssd_status apart = check_conv_areas(problem, x, weight, bias, state0, lengths, y0,
+                                              problem->split[1] ? y1 : nullptr,
+                                              problem->split[2] ? y2 : nullptr, stateT, false);
+    if (apart != SSD_OK) return apart;
     return status_of(ssd::launch_conv(conv_shape(problem), x, weight, bias, state0, lengths, y0,
                                       y1, y2, stateT, (hipStream_t)stream));
 }
@@ -165,6 +261,10 @@ ssd_status ssd_conv_step(const ssd_conv_problem *problem, const void *x, const f
         (problem->split[2] > 0 && !y2))
         return SSD_ERR_NULL_ARG;
     if (!on_bytes(16, {weight, bias})) return SSD_ERR_MISALIGNED;
+    const ssd_status apart = check_conv_areas(problem, x, weight, bias, nullptr, nullptr, y0,
+                                              problem->split[1] ? y1 : nullptr,
+                                              problem->split[2] ? y2 : nullptr, state, true);
+    if (apart != SSD_OK) return apart;
     return status_of(ssd::launch_conv_step(conv_shape(problem), x, weight, bias, state, y0, y1,
                                            y2, (hipStream_t)stream));
 }
@@ -191,6 +291,8 @@ ssd_status ssd_scan(const ssd_scan_problem *problem, const void *x, const void *
     st = check_scan_pointers(problem, A, B, C, {h0, hT, workspace});
     if (st != SSD_OK) return st;
     const ssd::ScanArgs a = {x, dt, A, B, C, D, z, dt_bias, h0, lengths, y, hT, workspace};
+    st = check_scan_areas(problem, a, hT, need > SSD_SCAN_NO_WORKSPACE ? need : 0, false);
+    if (st != SSD_OK) return st;
     return status_of(ssd::launch_scan(s, a, (hipStream_t)stream));
 }
 
@@ -205,6 +307,8 @@ ssd_status ssd_scan_step(const ssd_scan_problem *problem, const void *x, const v
     st = check_scan_pointers(problem, A, B, C, {h});
     if (st != SSD_OK) return st;
     const ssd::ScanArgs a = {x, dt, A, B, C, D, z, dt_bias, nullptr, nullptr, y, nullptr, nullptr};
+    st = check_scan_areas(problem, a, h, 0, true);
+    if (st != SSD_OK) return st;
     return status_of(ssd::launch_scan_step(scan_shape(problem), a, h, (hipStream_t)stream));
 }
 
@@ -214,10 +318,18 @@ ssd_status ssd_norm(const ssd_norm_problem *problem, const void *x, const void *
                     const void *residual, const float *weight, void *y, void *residual_out,
                     void *stream)
 {
-    const ssd_status st = check_norm(problem);
+    ssd_status st = check_norm(problem);
     if (st != SSD_OK) return st;
     if (!x || !weight || !y || (residual_out && !residual)) return SSD_ERR_NULL_ARG;
     if (!on_bytes(16, {weight})) return SSD_ERR_MISALIGNED;
+    // a lane writes the elements that it has read: outputs may be inputs of their own layout
+    const int64_t rows = problem->rows, width = problem->channels, e = bytes_of(problem->dtype);
+    const int64_t re = bytes_of(problem->residual_dtype);
+    st = check_apart({dense(y, rows * width * e), dense(residual_out, rows * width * re)},
+                     {rows_of(x, rows, problem->x_pitch, width, e, true),
+                      rows_of(z, rows, problem->z_pitch, width, e, true),
+                      dense(residual, rows * width * re, true), dense(weight, width * 4)});
+    if (st != SSD_OK) return st;
     ssd::NormShape s;
     s.rows = problem->rows; s.C = problem->channels; s.G = problem->ngroups;
     s.xp = problem->x_pitch ? problem->x_pitch : problem->channels;

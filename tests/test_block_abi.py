@@ -262,3 +262,98 @@ def test_row_layouts(shape, stride, lead, pitch):
             block._pitch(t, "t", lead)
     else:
         assert block._pitch(t, "t", lead) == pitch
+
+
+# ---------------------------------------------------------------------------
+# outputs apart from the other arguments: addresses far apart, but for the pair under test
+# (every call here is refused, so none of them is ever read)
+# ---------------------------------------------------------------------------
+def _far(n):
+    return [(i + 1) << 40 for i in range(n)]
+
+
+def _refused(fn, problem, ptrs, *tail):
+    args = [ctypes.c_void_p(p) for p in ptrs]
+    return fn(ctypes.byref(problem), *args, *tail, None) == 9
+
+
+def test_overlap_has_a_status():
+    assert "memory" in ssd.ssd_status_string(9) and binding.STATUS[9] == "SSD_ERR_OVERLAP"
+
+
+@pytest.mark.parametrize("out,other,off", [
+    (5, 0, 0),                     # y0 on x: a later token tile would read replaced rows
+    (5, 0, 200 * 320 * 2 - 16), (5, 0, 16 - 200 * 192 * 2),     # x's last and first 16 bytes
+    (6, 0, 4096), (7, 0, 64), (8, 0, 0), (5, 1, 0), (6, 2, 0), (7, 3, 0), (7, 4, 0), (6, 5, 0),
+    (7, 5, 256), (7, 6, 16), (8, 5, 0), (8, 7, 0), (8, 1, 0),
+    (8, 3, 16),                    # the final state in the state's buffer, but not at its start
+])
+def test_conv_outputs_apart(out, other, off):
+    # x, weight, bias, state0, lengths, y0, y1, y2, stateT
+    a = _far(9)
+    a[out] = a[other] + off
+    assert _refused(block.lib().ssd_conv, _conv(), a)
+
+
+def test_conv_output_between_rows_of_x():
+    """Rows of x are 320 of 1000 elements: what reaches into a row is refused."""
+    p = _conv(x_pitch=1000, batch=1, seqlen=3, split=(320, 0, 0))
+    a = _far(9)
+    for off in (638, 2000 - 1918, 2000, 2000 + 638, 2 * 2000 + 638, -2):
+        a[5] = a[0] + off
+        assert _refused(block.lib().ssd_conv, p, a), off
+
+
+@pytest.mark.parametrize("out,other,off", [
+    (4, 0, 2), (5, 0, 0), (6, 0, 0), (3, 0, 0), (3, 1, 0), (4, 1, 0), (5, 2, 0), (5, 3, 2), (5, 4, 64),
+    (4, 0, 0),                     # y0 at x's start, but narrower rows
+])
+def test_conv_step_outputs_apart(out, other, off):
+    # x, weight, bias, state, y0, y1, y2
+    a = _far(7)
+    a[out] = a[other] + off
+    assert _refused(block.lib().ssd_conv_step, _conv(seqlen=1), a)
+    # one output on a wider array's rows
+    a = _far(7)
+    a[4] = a[0]
+    assert _refused(block.lib().ssd_conv_step,
+                    _conv(seqlen=1, split=(320, 0, 0), x_pitch=328), a)
+
+
+@pytest.mark.parametrize("out,other,off", [
+    (10, 0, 0), (10, 1, 0), (10, 6, 0), (10, 3, 64), (10, 4, 0), (10, 2, 0), (10, 5, 0), (10, 7, 16),
+    (10, 8, 0), (10, 9, 0), (10, 11, 0), (10, 12, 0), (11, 0, 0), (11, 2, 0), (11, 8, 16), (11, 12, 0),
+    (12, 0, 0), (12, 8, 0), (12, 4, 1024), (11, 9, 0)])
+def test_scan_outputs_apart(out, other, off):
+    # x, dt, A, B, C, D, z, dt_bias, h0, lengths, y, hT, workspace
+    p = _scan(seqlen=1000)
+    a = _far(13)
+    a[out] = a[other] + off
+    assert _refused(block.lib().ssd_scan, p, a, ctypes.c_size_t(1 << 30))
+
+
+@pytest.mark.parametrize("out,other,off", [
+    (9, 0, 2), (9, 1, 16), (9, 6, -2), (9, 3, 0), (9, 4, 0), (9, 2, 0), (9, 8, 0), (8, 0, 0), (8, 2, 0),
+    (8, 4, 0), (8, 5, 0)])
+def test_scan_step_outputs_apart(out, other, off):
+    # x, dt, A, B, C, D, z, dt_bias, h, y
+    a = _far(10)
+    a[out] = a[other] + off
+    assert _refused(block.lib().ssd_scan_step, _scan(seqlen=1), a)
+    # groups so many that y and B are of one size: B's rows are still not y's
+    a = _far(10)
+    a[9] = a[3]
+    assert _refused(block.lib().ssd_scan_step, _scan(seqlen=1, channels=256, ngroups=16), a)
+
+
+@pytest.mark.parametrize("kw,out,other,off", [
+    ({}, 4, 0, 2), ({}, 4, 1, 512), ({}, 4, 3, 0), ({}, 5, 3, 0), ({}, 4, 5, 0), ({}, 5, 4, 0),
+    ({}, 4, 2, 0),                 # bf16 rows in a fp32 residual's buffer
+    ({}, 5, 0, 0),                 # and the other way round
+    (dict(residual_dtype=1), 5, 2, 16),
+    (dict(x_pitch=264), 4, 0, 0), (dict(z_pitch=512), 4, 1, 0)])
+def test_norm_outputs_apart(kw, out, other, off):
+    # x, z, residual, weight, y, residual_out
+    a = _far(6)
+    a[out] = a[other] + off
+    assert _refused(block.lib().ssd_norm, _norm(**kw), a)

@@ -810,3 +810,81 @@ def test_block_around_the_forward(dtype):
         err = ((ref.d64(got) - want).abs().max() / want.abs().max()).item()
         print(f"  {what}: {err:.2e}", flush=True)
         assert err <= tol, (what, err)
+
+
+# ---------------------------------------------------------------------------
+# shared memory: what is refused, and what the single-token forms and the norm allow
+# ---------------------------------------------------------------------------
+def test_outputs_in_inputs_are_refused():
+    """Before any launch: the inputs keep their values."""
+    dev = require_gpu()
+    x, w, bv, s0 = _conv_inputs("bf16", 2, 40, 64, 4, dev, 71)
+    d = _scan_inputs("bf16", 2, 40, 64, 1, 16, dev, 72)
+    kept = [t.clone() for t in (x, s0, d["x"], d["z"], d["h0"])]
+    long = {k: v.repeat_interleave(30, 1) if k in ("x", "dt", "B", "C", "z") else v for k, v in d.items()}
+    ws = torch.empty(1 << 24, device=dev, dtype=torch.uint8)
+    calls = [
+        lambda: ssd.ssd_conv(x, w, bv, s0, y=x),
+        lambda: ssd.ssd_conv(x[:1], w, bv, s0[:1], y=x.view(-1)[64:64 * 41].view(1, 40, 64)),
+        lambda: ssd.ssd_conv(x, w, bv, s0, split=[32, 32], y=[torch.empty(2, 40, 32, device=dev, dtype=x.dtype)] * 2),
+        lambda: ssd.ssd_conv(x, w, bv, x.view(-1)[:2 * 3 * 64].view(2, 3, 64), final_state=x.view(-1)[64:7 * 64].view(2, 3, 64)),
+        lambda: _run_scan(d, True, y=d["x"]),
+        lambda: _run_scan(d, True, y=d["z"]),
+        lambda: _run_scan(long, True, workspace=ws, hT=ws[1 << 10:].view(torch.float32)[:2 * 64 * 16].view(2, 64, 16)),
+        lambda: ssd.ssd_norm(d["x"], torch.ones(64, device=dev), residual=d["z"], y=d["x"], residual_out=d["x"]),
+    ]
+    for i, call in enumerate(calls):
+        with pytest.raises(ssd.SsdError) as err:
+            call()
+        assert err.value.status == 9, i
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(kept, (x, s0, d["x"], d["z"], d["h0"])))
+
+
+def test_outputs_between_the_rows_of_wide_inputs():
+    """A dense output in the columns next to a wider array's rows shares nothing with them."""
+    dev = require_gpu()
+    x, w, bv, s0 = _conv_inputs("bf16", 1, 3, 8, 4, dev, 73)
+    want, f0 = ssd.ssd_conv(x, w, bv, s0)
+    wide = torch.zeros(3, 64, device=dev, dtype=torch.bfloat16)
+    wide[:, 16:24] = x[0]
+    y = wide[0, 32:56].view(1, 3, 8)              # 24 elements between the rows of tokens 0 and 1
+    got, f1 = ssd.ssd_conv(wide[None, :, 16:24], w, bv, s0, y=y)
+    torch.cuda.synchronize()
+    assert got is y and torch.equal(got, want) and torch.equal(f0, f1)
+    assert torch.equal(wide[:, 16:24], x[0])
+
+
+@pytest.mark.parametrize("dtype,c", [("bf16", 96), ("fp32", 33), ("bf16", 20001)])
+def test_steps_and_norms_in_place(dtype, c):
+    """A step's and a norm's output in the buffer of x (or of the gate, the step sizes, the
+    residual stream): the bits of an output of its own."""
+    dev = require_gpu()
+    x, w, z, r = _norm_inputs(dtype, 37, c, "first", dtype, dev, 74)
+    for kw in (dict(z=z), dict(z=z, residual=r, scale=0.5), dict(z=z, gate_after=True)):
+        want = ssd.ssd_norm(x, w, **kw)
+        for k in ("x", "z") + (("residual",) if "residual" in kw else ()):
+            t = {"x": x, **kw}
+            t[k] = t[k].clone()
+            got = ssd.ssd_norm(weight=w, y=t[k], **t)
+            torch.cuda.synchronize()
+            both = zip(got, want) if "residual" in kw else ((got, want),)
+            assert all(torch.equal(p, q) for p, q in both), (kw.keys(), k)
+    if c > 10000:
+        return
+    x, w, bv, s0 = _conv_inputs(dtype, 5, 1, c, 4, dev, 75)
+    s1, a = s0.clone(), x[:, 0].clone()
+    want = ssd.ssd_conv_step(x[:, 0].clone(), w, bv, s0)
+    assert ssd.ssd_conv_step(a, w, bv, s1, y=a) is a
+    torch.cuda.synchronize()
+    assert torch.equal(a, want) and torch.equal(s0, s1)
+    d = _scan_inputs(dtype, 5, 1, c, 1, 16, dev, 76)
+    t = {k: d[k][:, 0].contiguous() for k in ("x", "dt", "B", "C", "z")}
+    h0 = d["h0"].clone()
+    want = ssd.ssd_scan_step(t["x"], t["dt"], d["A"], t["B"], t["C"], h0, z=t["z"], dt_softplus=True)
+    for k in ("x", "dt", "z"):
+        u, h1 = {**t, k: t[k].clone()}, d["h0"].clone()
+        got = ssd.ssd_scan_step(u["x"], u["dt"], d["A"], u["B"], u["C"], h1, z=u["z"],
+                                dt_softplus=True, y=u[k])
+        torch.cuda.synchronize()
+        assert got is u[k] and torch.equal(got, want) and torch.equal(h0, h1), k
