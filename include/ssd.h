@@ -411,11 +411,12 @@ ssd_status ssd_scan_step(const ssd_scan_problem *problem, const void *x, const v
  *     residual_out[r,c] = v    rounded to the residual's type (the norm takes the sum
  *                              itself, not the rounded one)
  *     y[r,c] = v / sqrt(mean_group(v^2) + eps) weight[c]
- *                              gate after (gate_after 1, z given): y *= z / (1 + exp(-z)) */
+ *                              gate after (gate_after 1, z given): y *= z / (1 + exp(-z))
+ * The group's sum of squares is an fp32 number: where it passes 2^128 it is infinite, and y 0. */
 typedef struct {
     int64_t rows, channels, ngroups;
     int64_t x_pitch, z_pitch;     /* 0: channels */
-    float eps;                    /* > 0, finite */
+    float eps;                    /* a normal number: finite, at least 2^-126 */
     float scale;                  /* finite; read with a residual only */
     int32_t gate_after;           /* 0 or 1 */
     int32_t dtype;                /* x, z, y */

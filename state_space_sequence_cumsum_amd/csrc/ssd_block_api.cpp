@@ -5,6 +5,7 @@
 
 #include <hip/hip_runtime.h>
 
+#include <cfloat>
 #include <initializer_list>
 
 #include "ssd_launch.h"
@@ -126,7 +127,8 @@ ssd_status check_norm(const ssd_norm_problem *p)
         return SSD_ERR_BAD_SHAPE;
     if (!is_dtype(p->dtype) || !is_flag(p->gate_after)) return SSD_ERR_UNSUPPORTED;
     if (p->residual_dtype != SSD_F32 && p->residual_dtype != p->dtype) return SSD_ERR_UNSUPPORTED;
-    if (!finite(p->eps) || !(p->eps > 0.0f) || !finite(p->scale)) return SSD_ERR_UNSUPPORTED;
+    // the hardware's reciprocal root takes a subnormal number for zero
+    if (!finite(p->eps) || !(p->eps >= FLT_MIN) || !finite(p->scale)) return SSD_ERR_UNSUPPORTED;
     if (p->channels > kMaxChannels || p->x_pitch > kMaxPitch || p->z_pitch > kMaxPitch ||
         p->rows > kMaxRows || p->rows > (kMaxGrid - 1) / p->ngroups)
         return SSD_ERR_UNSUPPORTED;

@@ -208,6 +208,13 @@ def test_norm_validate(kw, status):
         assert L.ssd_norm(ctypes.byref(p), *[OK16] * 6, None) == status
 
 
+@pytest.mark.parametrize("eps,status", [
+    (2.0 ** -126, 0), (1e-30, 0), (1e30, 0), (2.0 ** -127, 3), (1e-39, 3), (1e-45, 3), (1e-60, 3)])
+def test_norm_eps_is_a_normal_number(eps, status):
+    """A row of zeros has eps alone under its root, which takes a subnormal number for zero."""
+    assert block.lib().ssd_norm_validate(ctypes.byref(_norm(eps=eps))) == status
+
+
 def test_norm_pointer_checks():
     L, p = block.lib(), _norm()
     # x, z, residual, weight, y, residual_out

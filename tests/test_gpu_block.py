@@ -540,6 +540,22 @@ def test_norm_residual_in_place_and_zero_rows(c):
     assert (y0[2] == 0).all() and (v0[2] == 0).all()
 
 
+@pytest.mark.parametrize("dtype,c", [("fp32", 64), ("bf16", 2049), ("fp32", 20000)])
+def test_norm_smallest_eps(dtype, c):
+    """The smallest eps: rows of zeros, and of elements whose squares vanish next to it or not."""
+    dev = require_gpu()
+    x = torch.zeros(4, c, dtype=TD[dtype])
+    x[1], x[2, ::2], x[3, 1] = 1e-18, -1e-22, 3.0
+    w = torch.linspace(-2, 2, c)
+    y, ey, _, _ = ref.norm(x, w, eps=2.0 ** -126)
+    out = ssd.ssd_norm(x.to(dev), w.to(dev), eps=2.0 ** -126)
+    torch.cuda.synchronize()
+    assert (out[0] == 0).all()
+    # (the squares of row 2 are subnormal, 1e-44: as many digits of y as they have are not asked for)
+    ref.check(out[[0, 1, 3]], y[[0, 1, 3]], ey[[0, 1, 3]], "y")
+    assert torch.isfinite(out).all()
+
+
 def test_norm_takes_leading_dimensions():
     dev = require_gpu()
     x, w, z, _ = _norm_inputs("bf16", 12, 128, "first", None, dev, 14)
