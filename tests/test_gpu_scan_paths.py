@@ -1,5 +1,5 @@
 """GPU tests of the scan's paths by what selects them: segments of every rule of the split, chains
-over many segments.  Against the 64-bit recurrence, element
+over many segments, the one-launch form with many waves.  Against the 64-bit recurrence, element
 by element, with the roundings of a run's summed steps counted as they are made.
 
 Groups of few channels give many waves (each owns channels of one group) for little work."""
@@ -75,6 +75,37 @@ def test_split_scans(case, ragged):
         if b == 1:
             lengths = [128 * seg + 1]          # one segment, of one token, behind a chain's round
     _check(d, lengths, seg + 16, dev)
+
+
+# dtype, b, L, groups, channels a group, dstate, lanes of a channel
+SHORTS = [
+    # five or more waves, four lanes a channel: 2049 to 4096 waves of 16 tokens, every state size
+    ("bf16", 16, 200, 10, 2, 8, 4), ("fp32", 4, 200, 1, 700, 16, 4), ("bf16", 13, 256, 10, 2, 24, 4),
+    ("fp32", 13, 256, 10, 1, 32, 4), ("bf16", 8, 256, 1, 512, 32, 4), ("fp32", 26, 128, 10, 2, 40, 4),
+    ("bf16", 60, 65, 7, 3, 48, 4), ("fp32", 40, 97, 9, 1, 56, 4), ("bf16", 8, 128, 1, 700, 64, 4),
+    # eight lanes
+    ("bf16", 6, 256, 1, 70, 16, 8), ("fp32", 7, 241, 2, 9, 32, 8), ("bf16", 6, 128, 3, 10, 64, 8),
+    ("fp32", 6, 100, 2, 20, 40, 8),
+]
+
+
+@pytest.mark.parametrize("ragged", [False, True], ids=["dense", "ragged"])
+@pytest.mark.parametrize("case", SHORTS, ids=str)
+def test_one_launch_with_many_waves(case, ragged):
+    """Dense, and with lengths at and around the ends of a wave's 16 tokens, whole waves of the
+    workgroup behind them."""
+    dtype, b, L, G, cg, N, lanes = case
+    dev = require_gpu()
+    assert _segments(dtype, b, L, G, cg, N) == 1
+    waves = -(-L // 16)
+    four = waves * b * G * -(-cg // 16)
+    assert waves > 4 and (four <= 2048 if lanes == 8 else 2048 < four <= 4096)
+    d = _scan_inputs(dtype, b, L, G * cg, G, N, dev, 82)
+    lengths = None
+    if ragged:
+        ends = [L, 0, 1, 16, 17, 129, 31, L - 1, 64, 65, 80]
+        lengths = [min(ends[i % len(ends)] + i // len(ends), L) for i in range(b)]
+    _check(d, lengths, 16, dev)
 
 
 def test_long_prompt_of_the_listed_size():
