@@ -172,11 +172,6 @@ def prepare(case, seed):
         for name in ("x", "dt", "B", "C", "z"):
             if state.get(name) is not None:
                 state[name] = state[name][:, 0]
-    if state.get("lengths") is not None:
-        # rows behind a sequence's length are left as they were: a program that reads the whole
-        # padded batch keeps outputs that it has cleared once
-        widths = _split(case) if case["op"] == "conv" else [c]
-        state["y"] = [torch.zeros(b, L, w, device="cuda", dtype=td) for w in widths]
     if own:
         # a decode loop binds its tensors once and calls the plan for every token
         import state_space_sequence_cumsum_amd as ssd
@@ -305,17 +300,15 @@ def run(state):
     import state_space_sequence_cumsum_amd as ssd
     if op == "conv":
         y, last = ssd.ssd_conv(state["x"], state["weight"], state["bias"], state["state"],
-                               silu=case["silu"], lengths=state["lengths"], split=_split(case),
-                               y=state.get("y"))
+                               silu=case["silu"], lengths=state["lengths"], split=_split(case))
         return list(y) + [last]
     if op == "conv_step":
         y = state["plan"].run()
         return list(y) + [state["state"]]
     if op == "scan":
-        y = state["y"][0] if "y" in state else None
         return ssd.ssd_scan(state["x"], state["dt"], state["A"], state["B"], state["C"],
                             D=state["D"], z=state["z"], dt_bias=state["dt_bias"], h0=state["h"],
-                            dt_softplus=case["softplus"], lengths=state["lengths"], y=y)
+                            dt_softplus=case["softplus"], lengths=state["lengths"])
     if op == "scan_step":
         return state["plan"].run(), state["h"]
     gate_after = case["gate"] == "after"
