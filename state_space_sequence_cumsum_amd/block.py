@@ -353,7 +353,8 @@ def ssd_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, *, dt_softpl
         if n > NO_WORKSPACE:
             workspace = _empty(n, torch.uint8, x.device, stream)
     else:
-        if workspace.get_device() != dev or not workspace.is_contiguous():
+        if not (isinstance(workspace, Tensor) and workspace.get_device() == dev
+                and workspace.is_contiguous()):
             raise ValueError("workspace must be a contiguous tensor on the inputs' device")
         n = workspace.numel() * workspace.element_size()
     _call(L.ssd_scan, (p, *ptrs, hp, lp, yp, tp, None if workspace is None else workspace.data_ptr(),

@@ -739,6 +739,14 @@ def test_refusals():
     assert abs(float(y[0, 0]) - 1) < 1e-4
 
 
+@pytest.mark.parametrize("workspace", [1 << 20, [0], "4096", b"0"], ids=repr)
+def test_workspace_that_is_no_tensor_is_refused(workspace):
+    dev = require_gpu()
+    d = _scan_inputs("bf16", 1, 1000, 64, 1, 16, dev, 77)
+    with pytest.raises(ValueError, match="workspace"):
+        _run_scan(d, True, workspace=workspace)
+
+
 def test_step_plans_and_graph():
     """ConvStepPlan and ScanStepPlan captured into one decode graph, inputs refilled between
     the replays: the states and outputs of the eager steps, bit for bit."""

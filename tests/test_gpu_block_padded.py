@@ -52,6 +52,25 @@ def test_scan_allocates_zeros_behind_sequences(L):
     assert torch.equal(y, given) and torch.equal(h0, h1)
 
 
+def test_zeros_on_a_given_stream():
+    """The clearing runs on the call's own stream, before its kernels."""
+    dev = require_gpu()
+    L, split, lengths = 4000, [256, 32], [4000, 7]
+    x, w, bias, s0 = _conv_inputs("bf16", 2, L, 288, 4, dev, 66)
+    lt = torch.tensor(lengths, dtype=torch.int32, device=dev)
+    want = [torch.zeros(2, L, m, device=dev, dtype=x.dtype) for m in split]
+    ssd.ssd_conv(x, w, bias, s0, lengths=lt, split=split, y=want)
+    side = torch.cuda.Stream(dev)
+    torch.cuda.synchronize()
+    for handle in (side, side.cuda_stream):
+        for _ in range(5):
+            with torch.cuda.stream(side):
+                _fill_free_memory(dev, x.dtype, 2 * L * 288 + 256)
+            ys, _ = ssd.ssd_conv(x, w, bias, s0, lengths=lt, split=split, stream=handle)
+            side.synchronize()
+            assert all(torch.equal(p, q) for p, q in zip(ys, want))
+
+
 def test_padded_calls_in_a_graph():
     """Captured, every replay clears the rows behind the sequences of that replay's lengths."""
     dev = require_gpu()
