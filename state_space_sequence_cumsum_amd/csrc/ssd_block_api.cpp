@@ -166,8 +166,11 @@ bool meet(const Area &out, const Area &in)
     if (out.p == nullptr || in.p == nullptr) return false;
     // the output's start from the input's, and the input's first row that ends behind it
     const int64_t d = (int64_t)(reinterpret_cast<uintptr_t>(out.p) - reinterpret_cast<uintptr_t>(in.p));
-    const int64_t row = d < in.width ? 0 : (d - in.width) / in.pitch + 1;
-    if (row >= in.rows || row * in.pitch >= d + out.width) return false;
+    if (d + out.width <= 0) return false;
+    if (d >= in.width) {
+        const int64_t row = in.rows == 1 ? 1 : (d - in.width) / in.pitch + 1;
+        if (row >= in.rows || row * in.pitch >= d + out.width) return false;
+    }
     return !(in.same && d == 0 && in.rows == 1 && in.width == out.width);
 }
 
