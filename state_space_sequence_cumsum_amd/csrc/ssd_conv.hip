@@ -11,7 +11,7 @@
 // and C columns of a block's projection come out as ssd_forward takes them.
 //
 // Measured (inputs not in the caches): 16384 x 2560 bf16, a slice of rows of 4640, 39 to 41 us
-// (4.2 TB/s; a 1 GiB copy reaches 5.1), 262144 x 1536 bf16 299 us (5.4 TB/s), 5 x 2500 x 777
+// (4.2 TB/s; a copy kernel reaches 6.2), 262144 x 1536 bf16 299 us (5.4 TB/s), 5 x 2500 x 777
 // bf16 one channel a thread 14.0 us (2.8 TB/s); 256 x 384 fp32 4.2 us, most of it the launch.
 
 #include <hip/hip_runtime.h>
@@ -237,8 +237,10 @@ hipError_t conv_go(const ConvShape &s, const void *x, const float *w, const floa
                    void *stateT, hipStream_t st)
 {
     const int groups = (int)(s.C / V);
-    // Tokens per thread: 32, fewer where that leaves under 16 waves a CU; below 8 the halo costs
-    // what the threads gain (2 x 2048 x 1792: 14.2 us with 4, 11.2 with 8).
+    // Tokens per thread: 32, fewer where that leaves under 16 waves a CU (for 16 bytes a thread one
+    // to two rounds of what is resident: bf16 with four taps takes 171 registers, two waves a SIMD,
+    // three taps 139, two 97); below 8 the halo costs what the threads gain (2 x 2048 x 1792: 14.2 us
+    // with 4, 11.2 with 8).
     constexpr int64_t kWanted = 256 * 16 * 64;
     int tt = 32;
     while (tt > 8 && groups * ((s.L + tt - 1) / tt) * s.b < kWanted) tt /= 2;

@@ -11,9 +11,9 @@
 // in registers.
 //
 // Measured (inputs not in the caches): gated norm of 16384 x 2048 bf16, z a slice of rows of
-// 4640, 42 us (4.8 TB/s; a 1 GiB copy reaches 5.1; read twice by a workgroup a row: 143 us),
+// 4640, 42 us (4.8 TB/s; a copy kernel reaches 6.2; read twice by a workgroup a row: 143 us),
 // with a fp32 residual stream 77 us (5.2 TB/s), 3000 x 1001 bf16 in single elements 7.9 us
-// (2.3 TB/s), 128 x 1024 with residual 3.8 us, most of it the launch.
+// (2.3 TB/s), 128 x 1024 with residual 3.9 us, most of it the launch.
 #include <hip/hip_runtime.h>
 
 #include "ssd_device.h"
@@ -216,7 +216,10 @@ hipError_t norm_go(NormArgs<T, R> a, hipStream_t st)
 }
 
 // The smallest team that holds a group in its registers: part of a wave with one vector a lane,
-// a wave with up to 4 (16 single elements), a workgroup with up to 8 (16).
+// a wave with up to 4 (16 single elements), a workgroup with up to 8 (16).  Eight vectors of bf16
+// take all 256 registers and up to 45 accumulation registers, one wave a SIMD: gated rows of 16384
+// run at 3.6 TB/s, with a fp32 residual at 4.9, where rows of 8192 reach 5.5 and 5.0; rows that are
+// read twice (16392 channels) at 3.4 and 3.7.
 template <typename T, typename R, int V> hipError_t norm_team(NormArgs<T, R> a, hipStream_t st)
 {
     constexpr int kWave = V == 1 ? 16 : 4, kGroup = V == 1 ? 16 : 8;

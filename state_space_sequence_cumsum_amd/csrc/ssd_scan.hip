@@ -7,17 +7,19 @@
 //
 // A wave owns 64 channels of one group, a lane one of them, with its N states and rates in
 // registers; B_t and C_t, the same for all lanes, are broadcast from LDS.  Per state and token:
-// two products, an exp2 (two VALU slots on gfx950) and two fused multiply-adds (one without the
-// output), which bound the scan before HBM does.  Where the channels give too few waves, the
+// two products, an exp2 and two fused multiply-adds (one without the output), whose issue (four
+// cycles each; an exp2 alone takes eight, next to other waves' instructions six or seven) bounds
+// the scan before HBM does.  Where the channels give too few waves, the
 // tokens are split into segments: one launch scans each segment from zero for its end state, a
 // short one chains these into the segments' start states (exp of A times a segment's summed
 // steps is its factor), and one scans the segments again from there.  The first scan costs 0.8
 // of the second, and the bound is both.  Short prompts do the same within one workgroup and launch.
 //
-// Measured (bf16, 16384 tokens, 2048 channels, 16 states, gate and softplus): 204 to 209 us (96,
-// 128 and 16 us for the two scans and the chain, each profiled by itself); the VALU slots of the
-// two scans are 237 us at the 2.04 GHz of an fma loop, HBM's floor is 53 us.  One whole walk per
-// channel: 5.3 ms.
+// Measured (bf16, 16384 tokens, 2048 channels, 16 states, gate and softplus): 208 to 214 us (97 to
+// 99, 128 to 134 and 17 us for the two scans and the chain, each profiled by itself).  The scans
+// issue 44 and 58 thousand VALU instructions a SIMD, 176 and 231 thousand cycles; they take 190 to
+// 197 and 247 to 255 thousand, at clocks of 1.74 to 2.26 GHz read within the kernels (85 and 114 us
+// at the highest).  HBM's floor is 44 us.  One whole walk per channel: 5.3 ms.
 
 #include <hip/hip_runtime.h>
 
@@ -628,9 +630,12 @@ __global__ __launch_bounds__(256) void scan_step_kernel(
 // Segments that a sequence is split into, and tokens in each (a multiple of kStep); `waves`
 // waves of 64 channels would walk whole sequences.
 //   - From 1024 of them (one a SIMD) the sequences stay whole: the end states cost most of a
-//     second walk, which more waves then no longer make up for (16 x 4096 tokens, 4096 channels
-//     of 16 states: 1370 us whole, 1428 us in four segments; half as many sequences and channels,
-//     2048 tokens: 709 whole, 404 in eight).
+//     second walk, which more waves then no longer make up for.  2048 tokens of 4096 channels of 16
+//     states, whole and split, in us: 8 sequences (512 waves) 696 and 465, 12 (768) 699 and 649, 15
+//     (960) 696 and 784, 16 (1024) 692 and 790, 24 (1536) 985 and 1150, 32 (2048) 996 and 1454.  The
+//     rule does not know of lengths: ragged batches of those sizes gain from a split up to 2048 waves
+//     (686 and 278 at 512, 683 and 486 at 1024, 719 and 670 at 1536, 907 and 792 at 2048), so for
+//     them the border lies low, and for dense ones between 768 and 1024 a little high.
 //   - So do sequences under 32 tokens, where two more launches cost more than a walk (16 tokens:
 //     7.8 us whole, 12.0 split; 32 tokens: 13.0 and 12.1).
 //   - Else up to about 16384 waves of at least 64 tokens (30 ragged sequences of 1000 tokens, 2048
