@@ -363,7 +363,8 @@ ssd_status ssd_conv_step(const ssd_conv_problem *problem, const void *x, const f
  *     h_t[c,n] = exp(d_t[c] A[c,n]) h_{t-1}[c,n] + d_t[c] x[b,t,c] B[b,t,g,n]
  *     y[b,t,c] = (sum_n C[b,t,g,n] h_t[c,n] + D[c] x[b,t,c]) z / (1 + exp(-z))
  * with the last factor (the gate) only where z is given.  A token's own exp(d A) is an fp32
- * number (infinite from 2^128, zero below 2^-126); the factor of many tokens may be any. */
+ * number (infinite from 2^128, which makes a zero state NaN, and zero below 2^-126); the factor
+ * of many tokens may be any. */
 typedef struct {
     int64_t batch, seqlen, channels, ngroups, dstate;
     int64_t x_pitch, dt_pitch, z_pitch;   /* 0: channels */

@@ -17,8 +17,8 @@ pytestmark = pytest.mark.gpu
 def _segments(dtype, b, L, G, cg, N):
     """How many segments the library splits these sequences into, from its workspace: per
     segment N states and a sum of steps for each of 64 lanes of a wave (1: no workspace)."""
-    d = _scan_inputs(dtype, b, 1, G * cg, G, N, "cpu")
-    p = ssd.ScanProblem(b, L, G * cg, G, N, 0, 0, 0, 0, 0, 1, 1 if d["x"].dtype == torch.bfloat16 else 0)
+    p = ssd.ScanProblem(b, L, G * cg, G, N, 0, 0, 0, 0, 0, 1,
+                        ssd.SSD_BF16 if TD[dtype] == torch.bfloat16 else ssd.SSD_F32)
     n = ssd.ssd_scan_workspace_bytes(p)
     return 1 if n == 1 else n // (b * (N + 1) * G * -(-cg // 64) * 64 * 4)
 
