@@ -80,7 +80,7 @@ typedef enum {
                                  SSD_SCRATCH_BYTES of workspace                         */
     SSD_ERR_PLAN = 8,         /* a launch plan the kernels cannot run for the problem   */
     SSD_ERR_OVERLAP = 9       /* an output shares memory with another argument (checked by
-                                 the operators around the forward)                      */
+                                 the operators around the forward and linear attention)  */
 } ssd_status;
 
 typedef enum { SSD_F32 = 0, SSD_BF16 = 1 } ssd_dtype;
@@ -436,6 +436,99 @@ ssd_status ssd_norm_validate(const ssd_norm_problem *problem);
 ssd_status ssd_norm(const ssd_norm_problem *problem, const void *x, const void *z,
                     const void *residual, const float *weight, void *y, void *residual_out,
                     void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Linear attention with a decay for each head: the recurrence of ssd_forward for blocks whose
+ * queries, keys and decays stand by themselves (no step size that weighs a token, widths of
+ * keys and values other than 64s, padded batches), with its gradients.  For every head h, of group
+ * h / (nheads / ngroups), with a_t = exp(min(g_t, 0)),
+ *     S_t = a_t S_{t-1} + v_t k_t^T          o_t = scale S_t q_t
+ * The conventions of the operators around the forward hold, with these additions:
+ *   - q, k [b, L, ngroups, key_dim], v, o [b, L, nheads, value_dim] in `dtype`; states [b,
+ *     nheads, value_dim, key_dim] float32 (the layout of ssd_forward's, value rows).
+ *   - `decay` says what g holds: SSD_DECAY_NONE nothing (a = 1; g is not read and may be
+ *     NULL), SSD_DECAY_HEAD one log decay per head [nheads] float32, SSD_DECAY_TOKEN one
+ *     per token and head [b, L, nheads] in `dtype`.  A log decay above 0 is taken as 0, one of
+ *     minus infinity forgets everything before its token.
+ *   - q, k, v, do and their rows start on 16 bytes (pitches are multiples of 16 bytes), as do
+ *     outputs, states and the workspace; else SSD_ERR_MISALIGNED.
+ *   - states and sums are fp32.  For SSD_BF16 the decayed scores and the state that a chunk of
+ *     64 tokens reads are rounded to bf16 for the matrix products; what is added to a state
+ *     is not, so that states have fp32's precision.
+ *   - tokens go through in chunks of 64: a value that is not finite in q, k, v or do may make
+ *     NaN of any output of its chunk, not only of those that the recurrence leads to.
+ * ------------------------------------------------------------------------- */
+typedef enum { SSD_DECAY_NONE = 0, SSD_DECAY_HEAD = 1, SSD_DECAY_TOKEN = 2 } ssd_decay;
+
+typedef struct {
+    int64_t batch, seqlen, nheads, ngroups, key_dim, value_dim;
+    int64_t q_pitch, k_pitch;     /* 0: ngroups * key_dim */
+    int64_t v_pitch;              /* 0: nheads * value_dim */
+    int64_t g_pitch;              /* 0: nheads; read with SSD_DECAY_TOKEN only */
+    int64_t do_pitch;             /* 0: nheads * value_dim; read by the gradient only */
+    float scale;                  /* finite */
+    int32_t decay;                /* an ssd_decay value */
+    int32_t dtype;                /* q, k, v, o, per-token g, and their gradients */
+} ssd_linattn_problem;
+
+/* Host-only checks: dimensions positive, nheads divisible by ngroups, pitches 0 or at least the
+ * row's width, else SSD_ERR_BAD_SHAPE; key_dim and value_dim multiples of 8 up to 256, dtype
+ * and decay in their sets, scale finite, seqlen <= 2^30, batch * seqlen <= 2^31, batch * nheads
+ * <= 65535, pitches, nheads * value_dim and ngroups * key_dim <= 2^22 else SSD_ERR_UNSUPPORTED. */
+ssd_status ssd_linattn_validate(const ssd_linattn_problem *problem);
+
+/* Bytes of device workspace ssd_linattn needs; 0 if `problem` is not valid.  Host-only.  Up to
+ * SSD_LINATTN_NO_WORKSPACE means none: the workspace may then be NULL. */
+#define SSD_LINATTN_NO_WORKSPACE 1u
+size_t ssd_linattn_workspace_bytes(const ssd_linattn_problem *problem);
+
+/* Whole prompts.  h0 (the initial state), lengths and hT (the final state, which may be h0's
+ * buffer) may be NULL.  The workspace holds states of segments of long prompts and nothing
+ * between calls. */
+ssd_status ssd_linattn(const ssd_linattn_problem *problem, const void *q, const void *k,
+                       const void *v, const void *g, const float *h0, const int32_t *lengths,
+                       void *o, float *hT, void *workspace, size_t workspace_bytes, void *stream);
+
+/* One token per sequence (problem->seqlen must be 1, else SSD_ERR_BAD_SHAPE): q, k [b, ngroups,
+ * key_dim], v, o [b, nheads, value_dim], g [b, nheads], pitches from one sequence to the
+ * next; h is updated in place.  o may be v's buffer where that is dense.  Continues
+ * ssd_linattn's hT. */
+ssd_status ssd_linattn_step(const ssd_linattn_problem *problem, const void *q, const void *k,
+                            const void *v, const void *g, float *h, void *o, void *stream);
+
+/* Rotary positions, for the queries and keys of such a block: the first `rotated` elements of every
+ * head in pairs, (x_j, x_{j + rotated/2}), or (x_{2j}, x_{2j+1}) when interleaved, turned by
+ * position * freqs[j] radians and multiplied by scale:
+ *     (x, x') <- scale (x cos - x' sin, x' cos + x sin)
+ * The elements behind them go through unchanged.  `inverse` turns the other way (the gradient of
+ * the forward rotation).  Angles are formed and reduced in 64 bits.  Token t of sequence b has
+ * the position t (positions NULL; SSD_POSITIONS_START), positions[b] + t (SSD_POSITIONS_FIRST,
+ * [b]) or positions[b, t] (SSD_POSITIONS_EACH, [b, L]), int32. */
+typedef enum { SSD_POSITIONS_START = 0, SSD_POSITIONS_FIRST = 1, SSD_POSITIONS_EACH = 2 } ssd_positions;
+
+typedef struct {
+    int64_t batch, seqlen;
+    int64_t q_heads, k_heads;     /* k_heads 0: one array only */
+    int64_t head_dim, rotated;    /* rotated even, 0 < rotated <= head_dim */
+    int64_t q_pitch, k_pitch;     /* 0: heads * head_dim */
+    float scale;                  /* finite */
+    int32_t positions;            /* an ssd_positions value */
+    int32_t interleaved, inverse; /* 0 or 1 */
+    int32_t dtype;                /* q, k and the outputs */
+} ssd_rotary_problem;
+
+/* Host-only checks: dimensions positive (k_heads may be 0), rotated as described, pitches 0 or at
+ * least the row's width, else SSD_ERR_BAD_SHAPE; dtype, flags and positions in their sets, scale
+ * finite, head_dim <= 4096, heads * head_dim and pitches <= 2^22, seqlen <= 2^30, batch *
+ * seqlen < 2^24 else SSD_ERR_UNSUPPORTED. */
+ssd_status ssd_rotary_validate(const ssd_rotary_problem *problem);
+
+/* q [b, L, q_heads, head_dim], k [b, L, k_heads, head_dim] (NULL with k_heads 0); freqs
+ * [rotated / 2] float32; outputs dense, of the inputs' shapes, and may be the inputs' own buffers
+ * where those are dense. */
+ssd_status ssd_rotary(const ssd_rotary_problem *problem, const void *q, const void *k,
+                      const float *freqs, const int32_t *positions, void *q_out, void *k_out,
+                      void *stream);
 
 /* Static text for a status code. */
 const char *ssd_status_string(ssd_status status);

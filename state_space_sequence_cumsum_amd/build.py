@@ -14,8 +14,10 @@ SOURCES = [os.path.join(CSRC, "ssd_kernels.hip"), os.path.join(CSRC, "ssd_bf16.h
            os.path.join(CSRC, "ssd_step.hip"), os.path.join(CSRC, "ssd_noalloc.hip"),
            os.path.join(CSRC, "ssd_small.hip"),
            os.path.join(CSRC, "ssd_conv.hip"), os.path.join(CSRC, "ssd_scan.hip"),
-           os.path.join(CSRC, "ssd_norm.hip"),
-           os.path.join(CSRC, "ssd_api.cpp"), os.path.join(CSRC, "ssd_block_api.cpp")]
+           os.path.join(CSRC, "ssd_norm.hip"), os.path.join(CSRC, "ssd_linattn.hip"),
+           os.path.join(CSRC, "ssd_linattn_step.hip"), os.path.join(CSRC, "ssd_rotary.hip"),
+           os.path.join(CSRC, "ssd_api.cpp"), os.path.join(CSRC, "ssd_block_api.cpp"),
+           os.path.join(CSRC, "ssd_linattn_api.cpp")]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",

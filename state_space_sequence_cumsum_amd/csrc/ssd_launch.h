@@ -157,6 +157,39 @@ struct NormShape {
 hipError_t launch_norm(const NormShape &s, const void *x, const void *z, const void *residual,
                        const float *weight, void *y, void *residual_out, hipStream_t st);
 
+// ---------------------------------------------------------------------------
+// Linear attention with a decay for each head (ssd_linattn.hip, ssd_linattn_step.hip) and rotary
+// positions (ssd_rotary.hip); C entries in ssd_linattn_api.cpp.
+// ---------------------------------------------------------------------------
+struct LinattnShape {
+    int64_t b, L, H, G, dk, dv;
+    int64_t qp, kp, vp, gp, dop;
+    float scale;
+    int decay;              // an ssd_decay value
+    bool bf16;
+};
+struct LinattnArgs {
+    const void *q, *k, *v, *g;
+    const float *h0;         // may be NULL: zero
+    const int32_t *lengths;  // may be NULL: all L
+    void *o;
+    float *hT;               // may be NULL
+    void *ws;
+};
+hipError_t launch_linattn(const LinattnShape &s, const LinattnArgs &a, hipStream_t st);
+// One token per sequence (s.L = 1), h [b, H, dv, dk] updated in place.
+hipError_t launch_linattn_step(const LinattnShape &s, const LinattnArgs &a, float *h, hipStream_t st);
+
+struct RotaryShape {
+    int64_t b, L, Hq, Hk, D, rot;     // Hk 0: no second array
+    int64_t qp, kp;
+    float scale;
+    bool interleaved, inverse, bf16;
+    int positions;                    // 0: from 0, 1: first one of each sequence, 2: every token's
+};
+hipError_t launch_rotary(const RotaryShape &s, const void *q, const void *k, const float *freqs,
+                         const int32_t *positions, void *yq, void *yk, hipStream_t st);
+
 // bf16 kernels (ssd_bf16.hip)
 hipError_t launch_state_pass_bf16(const Shape &s, const void *x, const void *B, const float *G2,
                                   const float *dtT, const float *h0, void *S, float *hT,
