@@ -496,6 +496,19 @@ ssd_status ssd_linattn(const ssd_linattn_problem *problem, const void *q, const 
 ssd_status ssd_linattn_step(const ssd_linattn_problem *problem, const void *q, const void *k,
                             const void *v, const void *g, float *h, void *o, void *stream);
 
+/* Gradients of ssd_linattn: for the gradients do of o ([b, L, nheads, value_dim], `dtype`) and
+ * dhT of hT (float32, NULL: zero), those of q, k, v (dense, `dtype`, heads that share a q and k
+ * added up), of a per-token g (dg [b, L, nheads], `dtype`; 0 where g is above 0 or minus
+ * infinity; NULL: not wanted, and NULL it must be without SSD_DECAY_TOKEN) and of h0 (dh0 float32,
+ * NULL: not wanted).  h0 and lengths are those of the forward call (NULL as there); its outputs
+ * are not needed.  Rows of outputs behind a sequence's length are left as they were. */
+size_t ssd_linattn_backward_workspace_bytes(const ssd_linattn_problem *problem);
+ssd_status ssd_linattn_backward(const ssd_linattn_problem *problem, const void *dout, const void *q,
+                                const void *k, const void *v, const void *g, const float *h0,
+                                const float *dhT, const int32_t *lengths, void *dq, void *dk,
+                                void *dv, void *dg, float *dh0, void *workspace,
+                                size_t workspace_bytes, void *stream);
+
 /* Rotary positions, for the queries and keys of such a block: the first `rotated` elements of every
  * head in pairs, (x_j, x_{j + rotated/2}), or (x_{2j}, x_{2j+1}) when interleaved, turned by
  * position * freqs[j] radians and multiplied by scale:

@@ -15,7 +15,8 @@ from .block import (ConvProblem, ConvStepPlan, NormProblem, ScanProblem, ScanSte
                     ssd_conv, ssd_conv_step, ssd_norm, ssd_scan, ssd_scan_step,
                     ssd_scan_workspace_bytes)
 from .linattn import (LinattnProblem, LinattnStepPlan, RotaryProblem, linattn_problem,
-                      rotary_frequencies, ssd_linattn, ssd_linattn_step,
+                      rotary_frequencies, ssd_linattn, ssd_linattn_backward,
+                      ssd_linattn_backward_workspace_bytes, ssd_linattn_step,
                       ssd_linattn_workspace_bytes, ssd_rotary)
 from .tune import autotune
 
@@ -26,5 +27,6 @@ __all__ = ["FORWARD_EVENTS", "SSD_BF16", "SSD_F32", "ForwardPlan", "SsdError", "
            "workspace_for", "workspace_views", "ConvProblem", "ConvStepPlan", "NormProblem",
            "ScanProblem", "ScanStepPlan", "scan_problem", "ssd_conv", "ssd_conv_step", "ssd_norm",
            "ssd_scan", "ssd_scan_step", "ssd_scan_workspace_bytes", "LinattnProblem", "LinattnStepPlan",
-           "RotaryProblem", "linattn_problem", "rotary_frequencies", "ssd_linattn", "ssd_linattn_step",
+           "RotaryProblem", "linattn_problem", "rotary_frequencies", "ssd_linattn", "ssd_linattn_backward",
+           "ssd_linattn_backward_workspace_bytes", "ssd_linattn_step",
            "ssd_linattn_workspace_bytes", "ssd_rotary"]

@@ -177,6 +177,17 @@ struct LinattnArgs {
     void *ws;
 };
 hipError_t launch_linattn(const LinattnShape &s, const LinattnArgs &a, hipStream_t st);
+struct LinattnGradArgs {
+    const void *dout, *q, *k, *v, *g;
+    const float *h0, *dhT;   // may be NULL: zero
+    const int32_t *lengths;  // may be NULL: all L
+    void *dq, *dk, *dv;
+    void *dg;                // NULL: not wanted
+    float *dh0;              // NULL: not wanted
+    void *ws;
+};
+size_t linattn_backward_workspace_bytes(const LinattnShape &s);
+hipError_t launch_linattn_backward(const LinattnShape &s, const LinattnGradArgs &a, hipStream_t st);
 // One token per sequence (s.L = 1), h [b, H, dv, dk] updated in place.
 hipError_t launch_linattn_step(const LinattnShape &s, const LinattnArgs &a, float *h, hipStream_t st);
 

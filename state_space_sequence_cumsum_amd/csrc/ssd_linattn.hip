@@ -27,6 +27,7 @@
 // that states, which leave the kernel in fp32, hold fp32's precision.
 #include <hip/hip_runtime.h>
 
+#include "../../include/ssd.h"
 #include "ssd_device.h"
 #include "ssd_launch.h"
 
@@ -522,36 +523,37 @@ template <typename T>
 __global__ __launch_bounds__(kThreads) void decay_gradient_kernel(DecayGradient a)
 {
     const int lane = threadIdx.x & 63;
-    const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (id >= a.bh * a.nchunks) return;
-    const int64_t bh = id / a.nchunks;
-    const int c = (int)(id % a.nchunks);
-    const int64_t b = bh / a.H;
-    const int h = (int)(bh % a.H);
-    int n = a.L;
-    if (a.lengths) n = min(max(a.lengths[b], 0), a.L);
-    const int t = c * kChunk + lane;
-    if (c * kChunk >= n) return;
-    float read = 0.0f, written = 0.0f, cross = 0.0f;
-    for (int i = 0; i < a.nvb; ++i) {
-        if (t < n) {
-            read += a.read[(bh * a.nvb + i) * a.L + t];
-            written += a.written[(bh * a.nvb + i) * a.L + t];
+    for (int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); id < a.bh * a.nchunks;
+         id += (int64_t)gridDim.x * 4) {
+        const int64_t bh = id / a.nchunks;
+        const int c = (int)(id % a.nchunks);
+        const int64_t b = bh / a.H;
+        const int h = (int)(bh % a.H);
+        int n = a.L;
+        if (a.lengths) n = min(max(a.lengths[b], 0), a.L);
+        const int t = c * kChunk + lane;
+        if (c * kChunk >= n) continue;
+        float read = 0.0f, written = 0.0f, cross = 0.0f;
+        for (int i = 0; i < a.nvb; ++i) {
+            if (t < n) {
+                read += a.read[(bh * a.nvb + i) * a.L + t];
+                written += a.written[(bh * a.nvb + i) * a.L + t];
+            }
+            cross += a.cross[(bh * a.nvb + i) * a.nchunks + c];
         }
-        cross += a.cross[(bh * a.nvb + i) * a.nchunks + c];
-    }
-    const float before = wave_shift_up1(wave_inclusive_sum(written));
-    float suffix = read;
+        const float before = wave_shift_up1(wave_inclusive_sum(written));
+        float behind = read;                  // of this lane and those behind it
 #pragma unroll
-    for (int s = 1; s < 64; s <<= 1) {
-        const float up = __shfl_down(suffix, s, 64);
-        suffix += lane + s < 64 ? up : 0.0f;
+        for (int s = 1; s < 64; s <<= 1) {
+            const float up = __shfl_down(behind, s, 64);
+            behind += lane + s < 64 ? up : 0.0f;
+        }
+        if (t >= n) continue;
+        const float g = (float)((const T *)a.g)[(b * a.L + t) * a.gp + h];
+        float d = behind + before + cross;
+        if (g > 0.0f || g * kLog2e < -1000.0f) d = 0.0f;
+        ((T *)a.dg)[(b * a.L + t) * a.H + h] = Elem<T>::from_f32(d);
     }
-    if (t >= n) return;
-    const float g = (float)((const T *)a.g)[(b * a.L + t) * a.gp + h];
-    float d = suffix + before + cross;
-    if (g > 0.0f || g * kLog2e < -1000.0f) d = 0.0f;
-    ((T *)a.dg)[(b * a.L + t) * a.H + h] = Elem<T>::from_f32(d);
 }
 
 // Gradients of shared queries or keys: the sum of their heads', in the heads' order.
@@ -561,16 +563,24 @@ __global__ __launch_bounds__(kThreads) void shared_sum_kernel(const float *__res
                                                               const int32_t *__restrict__ lengths,
                                                               int64_t quads, int L, int G, int share, int kd)
 {
-    const int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    if (id >= quads) return;
     const int kq = kd / 4;
-    const int64_t row = id / kq;              // token and group
-    const int64_t token = row / G;
-    if (lengths && (int)(token % L) >= lengths[token / L]) return;
-    const float *p = per_head + row * share * kd + id % kq * 4;
-    f32x4 s = load4(p);
-    for (int i = 1; i < share; ++i) s += load4(p + (int64_t)i * kd);
-    store4(out + row * kd + id % kq * 4, s);
+    for (int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x; id < quads;
+         id += (int64_t)gridDim.x * kThreads) {
+        const int64_t row = id / kq;              // token and group
+        const int64_t token = row / G;
+        if (lengths && (int)(token % L) >= lengths[token / L]) continue;
+        const float *p = per_head + row * share * kd + id % kq * 4;
+        f32x4 s = load4(p);
+        for (int i = 1; i < share; ++i) s += load4(p + (int64_t)i * kd);
+        store4(out + row * kd + id % kq * 4, s);
+    }
+}
+
+// Workgroups for `work` items, `each` a workgroup: the last kernels' loops take what is beyond.
+unsigned groups_for(int64_t work, int each)
+{
+    const int64_t n = (work + each - 1) / each;
+    return (unsigned)(n < (1 << 20) ? n : (1 << 20));
 }
 
 template <typename T, int DK, bool REV, Kind KIND>
@@ -591,6 +601,34 @@ hipError_t walk_by_key(const Walk &a, int64_t bh, hipStream_t st)
 
 int blocks_of(int64_t values) { return (int)((values + kBlock - 1) / kBlock); }
 
+int chunks_of(const LinattnShape &s) { return (int)((s.L + kChunk - 1) / kChunk); }
+
+// Workspace of the gradients (byte offsets, on 256 bytes): with a decays' gradient the states
+// before each chunk and the parts that its kernel adds up; with shared heads every head's dq and dk.
+struct GradLayout {
+    int64_t states, read, written, cross, dq, dk, bytes;
+};
+GradLayout grad_layout(const LinattnShape &s, bool gates)
+{
+    GradLayout y;
+    int64_t at = 0;
+    const auto take = [&](bool wanted, int64_t bytes) {
+        const int64_t off = at;
+        if (wanted) at += (bytes + 255) / 256 * 256;
+        return off;
+    };
+    const int64_t bh = s.b * s.H, nvb = blocks_of(s.dk), nc = chunks_of(s);
+    y.states = take(gates, bh * nc * s.dk * s.dv * (s.bf16 ? 2 : 4));
+    y.read = take(gates, bh * nvb * s.L * 4);
+    y.written = take(gates, bh * nvb * s.L * 4);
+    y.cross = take(gates, bh * nvb * nc * 4);
+    const int64_t heads = s.b * s.L * s.H * s.dk * 4;
+    y.dq = take(s.H > s.G, heads);
+    y.dk = take(s.H > s.G, heads);
+    y.bytes = at;
+    return y;
+}
+
 template <typename T> hipError_t forward_go(const LinattnShape &s, const LinattnArgs &a, hipStream_t st)
 {
     Walk w = {};
@@ -607,11 +645,103 @@ template <typename T> hipError_t forward_go(const LinattnShape &s, const Linattn
     return walk_by_key<T, false, kOut>(w, s.b * s.H, st);
 }
 
+// Gradients: three walks (q's forward in time, then k's and v's back), the decays' from the parts
+// that the first two leave, shared heads' sums.
+template <typename T>
+hipError_t backward_go(const LinattnShape &s, const LinattnGradArgs &a, hipStream_t st)
+{
+    const GradLayout y = grad_layout(s, a.dg != nullptr);
+    char *ws = (char *)a.ws;
+    const auto at = [&](int64_t off) { return ws ? ws + off : nullptr; };
+    const int share = (int)(s.H / s.G);
+    const int64_t bh = s.b * s.H;
+    const bool gates = a.dg != nullptr;
+    hipError_t e;
+
+    Walk w = {};
+    w.g = a.g; w.gp = s.gp; w.decay = s.decay; w.lengths = a.lengths;
+    w.L = (int)s.L; w.H = (int)s.H;
+    w.nchunks = chunks_of(s);
+    w.states = at(y.states);
+    w.cross = (float *)at(y.cross);
+
+    Walk q = w;          // dq = scale S^T do
+    q.q = a.dout; q.qp = s.dop; q.qdiv = 1;
+    q.k = a.v; q.kp = s.vp; q.kdiv = 1;
+    q.v = a.k; q.vp = s.kp; q.vdiv = share;
+    q.o = share > 1 ? at(y.dq) : a.dq; q.o32 = share > 1;
+    q.init = a.h0; q.sv = 1; q.sk = s.dk;
+    q.inter = q.intra = s.scale; q.weight = 1.0f;
+    q.kd = (int)s.dv; q.vd = (int)s.dk; q.nvb = blocks_of(s.dk);
+    q.x = a.q; q.xp = s.qp; q.xdiv = share;
+    q.part = (float *)at(y.read);
+    e = gates ? walk_by_key<T, false, kDq>(q, bh, st) : walk_by_key<T, false, kOut>(q, bh, st);
+    if (e != hipSuccess) return e;
+
+    Walk k = w;          // dk = dS^T v, scale in dS
+    k.q = a.v; k.qp = s.vp; k.qdiv = 1;
+    k.k = a.dout; k.kp = s.dop; k.kdiv = 1;
+    k.v = a.q; k.vp = s.qp; k.vdiv = share;
+    k.o = share > 1 ? at(y.dk) : a.dk; k.o32 = share > 1;
+    k.init = a.dhT; k.sv = 1; k.sk = s.dk;
+    k.inter = 1.0f; k.intra = k.weight = s.scale;
+    k.kd = (int)s.dv; k.vd = (int)s.dk; k.nvb = blocks_of(s.dk);
+    k.x = a.k; k.xp = s.kp; k.xdiv = share;
+    k.part = (float *)at(y.written);
+    e = gates ? walk_by_key<T, true, kDk>(k, bh, st) : walk_by_key<T, true, kOut>(k, bh, st);
+    if (e != hipSuccess) return e;
+
+    Walk v = w;          // dv = dS k
+    v.q = a.k; v.qp = s.kp; v.qdiv = share;
+    v.k = a.q; v.kp = s.qp; v.kdiv = share;
+    v.v = a.dout; v.vp = s.dop; v.vdiv = 1;
+    v.o = a.dv;
+    v.init = a.dhT; v.sv = s.dk; v.sk = 1;
+    v.last = a.dh0;
+    v.inter = 1.0f; v.intra = v.weight = s.scale;
+    v.kd = (int)s.dk; v.vd = (int)s.dv; v.nvb = blocks_of(s.dv);
+    e = walk_by_key<T, true, kOut>(v, bh, st);
+    if (e != hipSuccess) return e;
+
+    if (gates) {
+        DecayGradient d = {};
+        d.g = a.g; d.gp = s.gp; d.lengths = a.lengths;
+        d.read = q.part; d.written = k.part; d.cross = w.cross;
+        d.dg = a.dg;
+        d.bh = bh; d.L = (int)s.L; d.H = (int)s.H; d.nvb = q.nvb; d.nchunks = w.nchunks;
+        hipLaunchKernelGGL((decay_gradient_kernel<T>), dim3(groups_for(bh * w.nchunks, 4)), dim3(kThreads),
+                           0, st, d);
+        e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    if (share > 1) {
+        const int64_t quads = s.b * s.L * s.G * (s.dk / 4);
+        for (int i = 0; i < 2; ++i) {
+            hipLaunchKernelGGL((shared_sum_kernel<T>), dim3(groups_for(quads, kThreads)), dim3(kThreads),
+                               0, st, (const float *)at(i ? y.dk : y.dq), (T *)(i ? a.dk : a.dq), a.lengths, quads, (int)s.L, (int)s.G, share, (int)s.dk);
+            e = hipGetLastError();
+            if (e != hipSuccess) return e;
+        }
+    }
+    return hipSuccess;
+}
+
 }  // namespace
 
 hipError_t launch_linattn(const LinattnShape &s, const LinattnArgs &a, hipStream_t st)
 {
     return s.bf16 ? forward_go<bf16>(s, a, st) : forward_go<float>(s, a, st);
+}
+
+size_t linattn_backward_workspace_bytes(const LinattnShape &s)
+{
+    const int64_t n = grad_layout(s, s.decay == SSD_DECAY_TOKEN).bytes;
+    return n ? (size_t)n : SSD_LINATTN_NO_WORKSPACE;
+}
+
+hipError_t launch_linattn_backward(const LinattnShape &s, const LinattnGradArgs &a, hipStream_t st)
+{
+    return s.bf16 ? backward_go<bf16>(s, a, st) : backward_go<float>(s, a, st);
 }
 
 }  // namespace ssd

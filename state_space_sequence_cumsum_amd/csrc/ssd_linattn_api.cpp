@@ -138,6 +138,44 @@ ssd_status ssd_linattn(const ssd_linattn_problem *problem, const void *q, const 
     return status_of(ssd::launch_linattn(linattn_shape(problem), a, (hipStream_t)stream));
 }
 
+size_t ssd_linattn_backward_workspace_bytes(const ssd_linattn_problem *problem)
+{
+    return check_linattn(problem) == SSD_OK ? ssd::linattn_backward_workspace_bytes(linattn_shape(problem))
+                                            : 0;
+}
+
+ssd_status ssd_linattn_backward(const ssd_linattn_problem *problem, const void *dout, const void *q,
+                                const void *k, const void *v, const void *g, const float *h0,
+                                const float *dhT, const int32_t *lengths, void *dq, void *dk,
+                                void *dv, void *dg, float *dh0, void *workspace,
+                                size_t workspace_bytes, void *stream)
+{
+    ssd_status st = check_linattn(problem);
+    if (st != SSD_OK) return st;
+    const ssd_linattn_problem &p = *problem;
+    if (!dout || !q || !k || !v || !dq || !dk || !dv || (!g && p.decay != SSD_DECAY_NONE))
+        return SSD_ERR_NULL_ARG;
+    if (dg && p.decay != SSD_DECAY_TOKEN) return SSD_ERR_UNSUPPORTED;
+    const size_t need = ssd_linattn_backward_workspace_bytes(problem);
+    const bool work = need > SSD_LINATTN_NO_WORKSPACE;
+    if (work && (workspace == nullptr || workspace_bytes < need)) return SSD_ERR_WORKSPACE;
+    if (!on_bytes(16, {dout, q, k, v, h0, dhT, dq, dk, dv, dh0, work ? workspace : nullptr}) ||
+        !rows_aligned(problem, {p.q_pitch, p.k_pitch, p.v_pitch, p.do_pitch}))
+        return SSD_ERR_MISALIGNED;
+    const int64_t e = bytes_of(p.dtype), rows = p.batch * p.seqlen;
+    const int64_t qk = p.ngroups * p.key_dim, vo = p.nheads * p.value_dim;
+    const Inputs in = inputs_of(problem, q, k, v, g);
+    const int64_t states = state_bytes(problem);
+    st = check_apart({dense(dq, rows * qk * e), dense(dk, rows * qk * e), dense(dv, rows * vo * e),
+                      dense(dg, rows * p.nheads * e), dense(dh0, states),
+                      dense(work ? workspace : nullptr, (int64_t)need)},
+                     {in.q, in.k, in.v, in.g, rows_of(dout, rows, p.do_pitch, vo, e), dense(h0, states),
+                      dense(dhT, states), dense(lengths, p.batch * 4)});
+    if (st != SSD_OK) return st;
+    const ssd::LinattnGradArgs a = {dout, q, k, v, g, h0, dhT, lengths, dq, dk, dv, dg, dh0, workspace};
+    return status_of(ssd::launch_linattn_backward(linattn_shape(problem), a, (hipStream_t)stream));
+}
+
 ssd_status ssd_linattn_step(const ssd_linattn_problem *problem, const void *q, const void *k,
                             const void *v, const void *g, float *h, void *o, void *stream)
 {

@@ -50,6 +50,9 @@ def lib():
         L.ssd_linattn_workspace_bytes.argtypes, L.ssd_linattn_workspace_bytes.restype = [ap], sz
         L.ssd_linattn.argtypes, L.ssd_linattn.restype = [ap] + [vp] * 9 + [sz, vp], st
         L.ssd_linattn_step.argtypes, L.ssd_linattn_step.restype = [ap] + [vp] * 7, st
+        L.ssd_linattn_backward_workspace_bytes.argtypes = [ap]
+        L.ssd_linattn_backward_workspace_bytes.restype = sz
+        L.ssd_linattn_backward.argtypes, L.ssd_linattn_backward.restype = [ap] + [vp] * 14 + [sz, vp], st
         L.ssd_rotary_validate.argtypes, L.ssd_rotary_validate.restype = [rp], st
         L.ssd_rotary.argtypes, L.ssd_rotary.restype = [rp] + [vp] * 7, st
         _lib = L
@@ -92,6 +95,11 @@ def linattn_problem(q, v, *, decay=DECAY_TOKEN, scale=1.0) -> LinattnProblem:
 def ssd_linattn_workspace_bytes(problem: LinattnProblem) -> int:
     """Bytes of workspace ssd_linattn needs (1: none); 0 when the problem is not valid."""
     return lib().ssd_linattn_workspace_bytes(ctypes.byref(problem))
+
+
+def ssd_linattn_backward_workspace_bytes(problem: LinattnProblem) -> int:
+    """Bytes of workspace ssd_linattn_backward needs (1: none); 0 when the problem is not valid."""
+    return lib().ssd_linattn_backward_workspace_bytes(ctypes.byref(problem))
 
 
 def _workspace(workspace, need, validate, problem, dev, device, stream, what):
@@ -142,6 +150,45 @@ def ssd_linattn(q, k, v, g=None, h0=None, *, scale=1.0, lengths=None, o=None, hT
                                   "ssd_linattn")
     _call(L.ssd_linattn, (p, *ptrs, hp, lp, op, tp, wp, n, _stream(stream, dev)), dev, "ssd_linattn")
     return o, hT
+
+
+def ssd_linattn_backward(do, q, k, v, g=None, h0=None, dhT=None, *, scale=1.0, lengths=None, dq=None,
+                         dk=None, dv=None, dg=None, dh0=None, want_dg=True, want_dh0=True,
+                         workspace=None, stream=None):
+    """Gradients of ssd_linattn's inputs from ``do`` [b, L, heads, value], that of its o (may be
+    a column slice), and ``dhT``, that of its hT (None: zeros).  The other inputs are the forward
+    call's; its outputs are not needed.
+
+    Returns (dq, dk, dv, dg, dh0), each of its input's shape and type: dg None without a per-token
+    g (fixed decays have no gradient here) or with want_dg False, dh0 None without an h0 or
+    with want_dh0 False.  Rows behind a sequence's length are left as they were in given
+    outputs and zeros in those allocated here."""
+    prob, dev, ptrs = _inputs(q, k, v, g, scale, 2)
+    td, device = q.dtype, q.device
+    dp, prob.do_pitch = _rows(do, "do", td, v.shape, dev, 2)
+    states = (prob.batch, prob.nheads, prob.value_dim, prob.key_dim)
+    hp = _dense(h0, "h0", torch.float32, states, dev)
+    tp = _dense(dhT, "dhT", torch.float32, states, dev)
+    lp = _dense(lengths, "lengths", torch.int32, (prob.batch,), dev)
+    make = torch.empty if lengths is None else torch.zeros
+    outs = []
+    for t, name, shape, dtype, want in (
+            (dq, "dq", q.shape, td, True), (dk, "dk", q.shape, td, True), (dv, "dv", v.shape, td, True),
+            (dg, "dg", v.shape[:3], td, want_dg and prob.decay == DECAY_TOKEN),
+            (dh0, "dh0", states, torch.float32, want_dh0 and h0 is not None)):
+        if t is not None:
+            _dense(t, name, dtype, shape, dev)
+        elif want:
+            t = _empty(shape, dtype, device, stream, make if name != "dh0" else torch.empty)
+        outs.append(t)
+    L, p = lib(), ctypes.byref(prob)
+    need = L.ssd_linattn_backward_workspace_bytes(p) if workspace is None else 0
+    workspace, wp, n = _workspace(workspace, need, L.ssd_linattn_validate, p, dev, device, stream,
+                                  "ssd_linattn_backward")
+    _call(L.ssd_linattn_backward,
+          (p, dp, *ptrs, hp, tp, lp, *[None if t is None else t.data_ptr() for t in outs], wp, n,
+           _stream(stream, dev)), dev, "ssd_linattn_backward")
+    return tuple(outs)
 
 
 def _step_args(q, k, v, h, g, scale, o, stream):

@@ -163,6 +163,101 @@ def test_rows_behind_a_sequence():
 
 
 # ---------------------------------------------------------------------------
+# gradients
+# ---------------------------------------------------------------------------
+def _grad_inputs(dtype, b, L, G, H, dk, dv, dev, decay, state, seed=20):
+    d = _inputs(dtype, b, L, G, H, dk, dv, dev, decay, state, seed)
+    gen = torch.Generator().manual_seed(seed + 1)
+    d["do"] = _columns(dev, torch.randn(b, L, H, dv, generator=gen).to(TD[dtype]))[0]
+    d["dhT"] = torch.randn(b, H, dv, dk, generator=gen).to(dev) if state else None
+    return d
+
+
+@pytest.mark.parametrize("case", CASES, ids=str)
+def test_gradients(case):
+    dtype, b, L, G, H, dk, dv, decay, state, lengths = case
+    dev = require_gpu()
+    d = _grad_inputs(dtype, b, L, G, H, dk, dv, dev, decay, state)
+    got = ssd.ssd_linattn_backward(**d, scale=dk ** -0.5, lengths=_lengths(lengths, dev))
+    torch.cuda.synchronize()
+    n = None if lengths is None else [min(max(m, 0), L) for m in lengths]
+    want = ref.backward(**d, scale=dk ** -0.5, lengths=n)
+    for name, x, (r, e) in zip(("dq", "dk", "dv", "dg", "dh0"), got, want):
+        if x is None:
+            assert name == "dg" and decay != "token" or name == "dh0" and not state
+            continue
+        if name != "dh0":
+            for i, m in enumerate(n or []):
+                r[i, m:], e[i, m:] = 0, 0
+        ref.check(x, r, e, name)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_gradients_of_decays_far_apart(dtype):
+    dev = require_gpu()
+    d = _grad_inputs(dtype, 2, 200, 2, 2, 64, 64, dev, "token", True)
+    gen = torch.Generator().manual_seed(4)
+    pick = torch.randint(0, 7, (2, 200, 2), generator=gen).to(dev)
+    sizes = torch.tensor([0.0, -0.001, -1.0, -30.0, -300.0, -1e30, 2.0], device=dev).to(TD[dtype])
+    d["g"] = sizes[pick]
+    d["g"][0, 70] = -float("inf")
+    got = ssd.ssd_linattn_backward(**d)
+    torch.cuda.synchronize()
+    want = ref.backward(**d, scale=1.0)
+    off = ((d["g"] > 0) | (d["g"] < -1000)).cpu()
+    want[3][0][off], want[3][1][off] = 0, 0
+    for name, x, (r, e) in zip(("dq", "dk", "dv", "dg", "dh0"), got, want):
+        ref.check(x, r, e, name)
+
+
+def test_gradients_match_differences():
+    """The forward call itself along random directions: fp32 values, summed in 64 bits."""
+    dev = require_gpu()
+    d = _grad_inputs("fp32", 1, 150, 1, 2, 16, 24, dev, "token", True)
+    d["g"] = (d["g"] - 0.01).contiguous()
+    do, dhT = d.pop("do"), d.pop("dhT")
+    grads = ssd.ssd_linattn_backward(do, **d, dhT=dhT, scale=0.25)
+
+    def value(args):
+        o, hT = ssd.ssd_linattn(**args, scale=0.25)
+        return ((o.double() * do).sum() + (hT.double() * dhT).sum()).item()
+
+    gen = torch.Generator().manual_seed(9)
+    for name, grad in zip(("q", "k", "v", "g", "h0"), grads):
+        x = d[name].contiguous()
+        step = torch.randn(x.shape, generator=gen).to(dev) * (2.0 ** -10 if name != "g" else 2.0 ** -12)
+        up, down = x + step, x - step
+        slope = value({**d, name: up}) - value({**d, name: down})
+        # what the values really moved by; third-order terms and fp32's sums: 1e-3 of the size
+        along = (grad.double() * (up.double() - down.double()))
+        assert abs(slope - along.sum().item()) <= 1e-3 * along.norm().item() + 1e-4 * abs(slope)
+
+
+def test_gradients_behind_a_sequence():
+    dev = require_gpu()
+    lengths = [130, 0, 64, 3]
+    d = _grad_inputs("bf16", 4, 130, 2, 4, 64, 40, dev, "token", True)
+    lt = _lengths(lengths, dev)
+    for n in ("q", "k", "v", "g", "do"):
+        d[n] = d[n].clone()
+    clean = ssd.ssd_linattn_backward(**d, lengths=lt)
+    for i, m in enumerate(lengths):
+        for n in ("q", "k", "v", "g", "do"):
+            d[n][i, m:] = float("nan")
+    given = {n: torch.full_like(t, 7.0) for n, t in zip(("dq", "dk", "dv", "dg", "dh0"), clean)}
+    got = ssd.ssd_linattn_backward(**d, lengths=lt, **given)
+    torch.cuda.synchronize()
+    for x, y, name in zip(got, clean, given):
+        assert x is given[name]
+        for i, m in enumerate(lengths):
+            if name == "dh0":
+                assert torch.equal(x, y) and torch.equal(x[1], d["dhT"][1])
+            else:
+                assert torch.equal(x[i, :m], y[i, :m])
+                assert (x[i, m:] == 7).all() and (y[i, m:] == 0).all()
+
+
+# ---------------------------------------------------------------------------
 # single tokens
 # ---------------------------------------------------------------------------
 @pytest.mark.parametrize("case", [

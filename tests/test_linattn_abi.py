@@ -32,7 +32,8 @@ def _rotary(**kw):
 
 def test_every_entry_point_is_declared_and_exported():
     names = {"ssd_linattn", "ssd_linattn_step", "ssd_linattn_validate",
-             "ssd_linattn_workspace_bytes", "ssd_rotary", "ssd_rotary_validate"}
+             "ssd_linattn_workspace_bytes", "ssd_linattn_backward",
+             "ssd_linattn_backward_workspace_bytes", "ssd_rotary", "ssd_rotary_validate"}
     assert names <= set(binding.header_functions())
     assert all(hasattr(linattn.lib(), n) for n in names)
 
@@ -85,6 +86,42 @@ def test_linattn_validate(kw, status):
     if status:      # the entry points refuse the same problems
         assert L.ssd_linattn(ctypes.byref(p), *[OK16] * 9, 1 << 50, None) == status
         assert L.ssd_linattn_step(ctypes.byref(p), *[OK16] * 6, None) == status
+        assert L.ssd_linattn_backward(ctypes.byref(p), *[OK16] * 14, 1 << 50, None) == status
+    assert (ssd.ssd_linattn_backward_workspace_bytes(p) > 0) == (status == 0)
+
+
+def test_gradient_pointer_checks():
+    L, p = linattn.lib(), _problem()
+    n = ssd.ssd_linattn_backward_workspace_bytes(p)
+    assert n > 1 and ssd.ssd_linattn_backward_workspace_bytes(_problem(ngroups=8, decay=1)) == 1
+    # do, q, k, v, g, h0, dhT, lengths, dq, dk, dv, dg, dh0, workspace
+    for missing in (0, 1, 2, 3, 4, 8, 9, 10):
+        a = [OK16] * 14
+        a[missing] = None
+        assert L.ssd_linattn_backward(ctypes.byref(p), *a, n, None) == 1
+    assert L.ssd_linattn_backward(ctypes.byref(p), *[OK16] * 13, None, n, None) == 4
+    assert L.ssd_linattn_backward(ctypes.byref(p), *[OK16] * 14, n - 1, None) == 4
+    for off in (0, 1, 2, 3, 5, 6, 8, 9, 10, 12, 13):
+        a = [OK16] * 14
+        a[off] = OFF8
+        assert L.ssd_linattn_backward(ctypes.byref(p), *a, n, None) == 6
+    for pitch in ("q_pitch", "k_pitch", "v_pitch", "do_pitch"):
+        assert L.ssd_linattn_backward(ctypes.byref(_problem(**{pitch: 1028})), *[OK16] * 14, 1 << 40, None) == 6
+    # decays that are not given per token have no gradient
+    for decay in (0, 1):
+        assert L.ssd_linattn_backward(ctypes.byref(_problem(decay=decay)), *[OK16] * 14, n, None) == 3
+    assert L.ssd_linattn_backward(None, *[OK16] * 14, n, None) == 1
+    assert L.ssd_linattn_backward_workspace_bytes(None) == 0
+
+
+@pytest.mark.parametrize("out", [8, 9, 10, 11, 12, 13])
+def test_gradient_outputs_apart(out):
+    # do, q, k, v, g, h0, dhT, lengths, dq, dk, dv, dg, dh0, workspace
+    for other in range(14):
+        if other != out:
+            a = _far(14)
+            a[out] = a[other]
+            assert _refused(linattn.lib().ssd_linattn_backward, _problem(), a, ctypes.c_size_t(1 << 40))
 
 
 def test_linattn_pointer_checks():
@@ -219,6 +256,8 @@ def test_binding_refuses_host_tensors():
         ssd.ssd_linattn(q, q, v)
     with pytest.raises(ValueError):
         ssd.LinattnStepPlan(q[:, 0], q[:, 0], v[:, 0], torch.zeros(1, 2, 8, 8))
+    with pytest.raises(ValueError):
+        ssd.ssd_linattn_backward(v, q, q, v)
     with pytest.raises(ValueError):
         ssd.ssd_rotary(q, None, torch.ones(4))
     for t in (torch.zeros(1, 4, 2, 8, dtype=torch.float16), None, 3):
