@@ -176,6 +176,7 @@ struct LinattnArgs {
     float *hT;               // may be NULL
     void *ws;
 };
+size_t linattn_workspace_bytes(const LinattnShape &s);
 hipError_t launch_linattn(const LinattnShape &s, const LinattnArgs &a, hipStream_t st);
 struct LinattnGradArgs {
     const void *dout, *q, *k, *v, *g;

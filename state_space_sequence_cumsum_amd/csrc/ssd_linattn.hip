@@ -38,9 +38,9 @@ constexpr int kChunk = 64;       // tokens of a chunk
 constexpr int kBlock = 64;       // values of a walk
 constexpr int kThreads = 256;    // four waves
 
-// What a walk is run for: an output (of the forward, or the gradient of v), or the gradient of q
-// or k with its part of the decays' gradient.
-enum Kind { kOut, kDq, kDk };
+// What a walk is run for: the state that a segment of chunks leaves, from zero; an output (of the
+// forward, or the gradient of v); the gradient of q or k with its part of the decays' gradient.
+enum Kind { kEnds, kOut, kDq, kDk };
 
 // A walk's arrays, in the roles of the forward.
 struct Walk {
@@ -56,9 +56,16 @@ struct Walk {
     const float *init;          // value v, key k of a head at v sv + k sk; may be NULL
     int64_t sv, sk;
     float *last;                // [b, H, vd, kd]; may be NULL
+    // Segments: `seg` chunks each, nseg of them, in the walk's order.  With more than one, kEnds
+    // leaves their ends (from zero) and decays, a chain over those their starts, for the others.
+    int seg, nseg;
+    float *ends;                // [b H, nseg, vd kd] in init's layout: segment s's end at s + 1, then
+                                // its start at s
+    float *decays;              // [b H, nseg]: over segment s
     float inter, intra;         // factors of an output's two parts
     float weight;               // factor of what is added to the state
     int L, H, kd, vd, nvb;
+    int64_t groups;             // heads x segments
     // kDq, kDk: the array whose product with the output the decays' gradient takes (q, k), this
     // walk's part of it, and the states before each chunk, [b H, chunks, vd, kd]
     const void *x;
@@ -190,6 +197,20 @@ __device__ __forceinline__ f32x4 load4(const bf16 *p)
 }
 __device__ __forceinline__ f32x4 load4(const float *p) { return *reinterpret_cast<const f32x4 *>(p); }
 
+// The same through a buffer, past whose end nothing is written.
+__device__ __forceinline__ void buf_store4(rsrc_t r, uint32_t off, const f32x4 &v, bf16 *)
+{
+    u32x2 w;
+    w[0] = pack_bf16(v[0], v[1]);
+    w[1] = pack_bf16(v[2], v[3]);
+    __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(__attribute__((ext_vector_type(2))) unsigned int, w), r,
+                                          (int)off, 0, 0);
+}
+__device__ __forceinline__ void buf_store4(rsrc_t r, uint32_t off, const f32x4 &v, float *)
+{
+    buf_store_b128(r, off, __builtin_bit_cast(u32x4, v));
+}
+
 // A token's log decay in base 2, between -1000 and 0; a NaN stays one.
 __device__ __forceinline__ float decay2(float g)
 {
@@ -239,42 +260,55 @@ __global__ __launch_bounds__(kThreads, DK * sizeof(T) <= 256 ? 2 : 1) void walk_
     __shared__ __attribute__((aligned(16))) float sHi[kChunk], sLo[kChunk], sIn[kChunk], sW[kChunk];
     __shared__ float sZ[kChunk], sC[4][kChunk], sX[4];
 
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int c16 = lane & 15, g4 = lane >> 4;
-    const int vb = blockIdx.x % a.nvb;
-    const int64_t bh = blockIdx.x / a.nvb;
+    // workgroups are dealt to the 8 XCDs in turn: the blocks of values of one segment go to the same
+    // one, whose L2 then holds the q and k that they share
+    const int64_t group = (int64_t)(blockIdx.x / (8 * a.nvb)) * 8 + blockIdx.x % 8;
+    const int vb = blockIdx.x / 8 % a.nvb;
+    const int walks = KIND == kEnds ? a.nseg - 1 : a.nseg;
+    if (group >= a.groups) return;
+    const int64_t bh = group / walks;
+    const int s = (int)(group % walks);
     const int64_t b = bh / a.H;
     const int h = (int)(bh % a.H);
     const int v0 = vb * kBlock;
     int n = a.L;
     if (a.lengths) n = min(max(a.lengths[b], 0), a.L);
     const int nc = (n + kChunk - 1) / kChunk;
+    const int it0 = min(s * a.seg, nc), it1 = min(it0 + a.seg, nc);     // in the walk's order
 
     const int64_t row0 = b * a.L;
     const T *qb = (const T *)a.q + row0 * a.qp + (int64_t)(h / a.qdiv) * a.kd;
     const T *kb = (const T *)a.k + row0 * a.kp + (int64_t)(h / a.kdiv) * a.kd;
     const T *vbp = (const T *)a.v + row0 * a.vp + (int64_t)(h / a.vdiv) * a.vd + v0;
-    const T *xb = KIND == kOut ? nullptr
-                               : (const T *)a.x + row0 * a.xp + (int64_t)(h / a.xdiv) * a.vd + v0;
+    const T *xb = KIND == kDq || KIND == kDk
+                      ? (const T *)a.x + row0 * a.xp + (int64_t)(h / a.xdiv) * a.vd + v0
+                      : nullptr;
     const int vw = min(a.vd - v0, kBlock);
 
     // the state's accumulators: column the wave's value, rows 16 keys each
     const int val = 16 * wave + c16;
     const bool has_val = val < vw;
+    const int64_t size = (int64_t)a.kd * a.vd;
     f32x4 S[KT];
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt) {
         S[kt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         const int key = 16 * kt + 4 * g4;
-        if (a.init && has_val && key < a.kd) {
-            const float *p = a.init + bh * a.kd * a.vd + (int64_t)(v0 + val) * a.sv + (int64_t)key * a.sk;
+        if (!has_val || key >= a.kd) continue;
+        const int64_t at = (int64_t)(v0 + val) * a.sv + (int64_t)key * a.sk;
+        const float *p = KIND == kEnds   ? nullptr
+                         : a.nseg > 1    ? a.ends + (bh * a.nseg + s) * size + at
+                         : a.init        ? a.init + bh * size + at
+                                         : nullptr;
+        if (p)
 #pragma unroll
             for (int r = 0; r < 4; ++r) S[kt][r] = p[r * a.sk];
-        }
     }
 
     u32x4 kr[KI], vr[VI];
-    Key qn[KK];
+    Key qn[KIND == kEnds ? 1 : KK];
     float gn = 0.0f;
     const auto fetch = [&](int c) {
         const int t0 = c * kChunk, rows = min(kChunk, n - t0);
@@ -291,20 +325,35 @@ __global__ __launch_bounds__(kThreads, DK * sizeof(T) <= 256 ? 2 : 1) void walk_
             const int p = tid + i * kThreads, row = p / (kBlock / kVec), col = p % (kBlock / kVec) * kVec;
             vr[i] = buf_load_b128(rv, col < vw ? (uint32_t)((row * (int)a.vp + col) * (int)sizeof(T)) : ~0u);
         }
+        if constexpr (KIND != kEnds) {
 #pragma unroll
-        for (int kk = 0; kk < KK; ++kk) {
-            const int col = Tile<T>::kKeys * kk + Tile<T>::kStepKeys * g4;
-            qn[kk] = __builtin_bit_cast(Key, buf_load_b128(rq, col < a.kd
-                ? (uint32_t)(((16 * wave + c16) * (int)a.qp + col) * (int)sizeof(T)) : ~0u));
+            for (int kk = 0; kk < KK; ++kk) {
+                const int col = Tile<T>::kKeys * kk + Tile<T>::kStepKeys * g4;
+                qn[kk] = __builtin_bit_cast(Key, buf_load_b128(rq, col < a.kd
+                    ? (uint32_t)(((16 * wave + c16) * (int)a.qp + col) * (int)sizeof(T)) : ~0u));
+            }
         }
         gn = 0.0f;
         if (a.decay != 0 && lane < rows)
             gn = a.decay == 1 ? ((const float *)a.g)[h]
                               : (float)((const T *)a.g)[(row0 + t0 + lane) * a.gp + h];
     };
-    if (nc > 0) fetch(REV ? nc - 1 : 0);
+    // rows of the outputs (those behind the sequence and values behind the block dropped)
+    const auto store_out = [&](auto *base, int t0, int rows, int i, const f32x4 (&o)[4]) {
+        typedef std::remove_pointer_t<decltype(base)> O;
+        const int pitch = a.H * a.vd;
+        const rsrc_t ro = make_rsrc(base + ((row0 + t0) * a.H + h) * a.vd + v0,
+                                    ((rows - 1) * pitch + vw) * (int)sizeof(O));
+#pragma unroll
+        for (int vt = 0; vt < 4; ++vt) {
+            const int v = 16 * vt + 4 * g4;
+            buf_store4(ro, v < vw ? (uint32_t)((i * pitch + v) * (int)sizeof(O)) : ~0u, o[vt], (O *)nullptr);
+        }
+    };
+    if (it0 < it1) fetch(REV ? nc - 1 - it0 : it0);
 
-    for (int it = 0; it < nc; ++it) {
+    float passed = 1.0f;      // the decay over the segment
+    for (int it = it0; it < it1; ++it) {
         const int c = REV ? nc - 1 - it : it;
         const int t0 = c * kChunk, rows = min(kChunk, n - t0);
         // the chunk into LDS: K, V, the state as the products read it, and the factors
@@ -318,17 +367,20 @@ __global__ __launch_bounds__(kThreads, DK * sizeof(T) <= 256 ? 2 : 1) void walk_
             const int p = tid + i * kThreads, row = p / (kBlock / kVec), col = p % (kBlock / kVec) * kVec;
             *reinterpret_cast<u32x4 *>(sV + row * VP + col) = vr[i];
         }
+        Key q[KIND == kEnds ? 1 : KK];
+        if constexpr (KIND != kEnds) {
 #pragma unroll
-        for (int kt = 0; kt < KT; ++kt) store4(sS + val * SP + 16 * kt + 4 * g4, S[kt]);
-        Key q[KK];
+            for (int kt = 0; kt < KT; ++kt) store4(sS + val * SP + 16 * kt + 4 * g4, S[kt]);
 #pragma unroll
-        for (int kk = 0; kk < KK; ++kk) q[kk] = qn[kk];
+            for (int kk = 0; kk < KK; ++kk) q[kk] = qn[kk];
+        }
         const float g2 = decay2(gn);
         const float ghi = __builtin_rintf(g2 * 256.0f) * (1.0f / 256.0f);
         const float hi = wave_inclusive_sum(ghi), lo = wave_inclusive_sum(g2 - ghi);
         const float hE = wave_read(hi, 63), lE = wave_read(lo, 63);
         const float from_start = fast_exp2(hi + lo), to_end = fast_exp2((hE - hi) + (lE - lo));
         const float whole = fast_exp2(hE + lE);
+        if (KIND == kEnds) passed *= whole;
         if (wave == 0) {
             sHi[lane] = hi;
             sLo[lane] = lo;
@@ -336,137 +388,135 @@ __global__ __launch_bounds__(kThreads, DK * sizeof(T) <= 256 ? 2 : 1) void walk_
             sW[lane] = (REV ? from_start : to_end) * a.weight;
         }
         __syncthreads();
-        if (it + 1 < nc) fetch(REV ? c - 1 : c + 1);
+        if (it + 1 < it1) fetch(REV ? c - 1 : c + 1);
 
-        // what the state before the chunk gives
-        const int i = 16 * wave + c16;                     // this lane's target
-        f32x4 o[4] = {};
+        if constexpr (KIND != kEnds) {
+            // what the state before the chunk gives
+            const int i = 16 * wave + c16;                     // this lane's target
+            f32x4 o[4] = {};
 #pragma unroll
-        for (int kk = 0; kk < KK; ++kk)
+            for (int kk = 0; kk < KK; ++kk)
 #pragma unroll
-            for (int vt = 0; vt < 4; ++vt) {
-                const Key s = *reinterpret_cast<const Key *>(
-                    sS + (16 * vt + c16) * SP + Tile<T>::kKeys * kk + Tile<T>::kStepKeys * g4);
-                o[vt] = mma16(s, q[kk], o[vt]);
-            }
-        const float in = sIn[i];
-#pragma unroll
-        for (int vt = 0; vt < 4; ++vt) o[vt] *= in;
-
-        // partner rows of the gradient of the decays
-        float part = 0.0f;
-        Key xf[KIND == kDq ? BK : 1];
-        if constexpr (KIND != kOut) {
-            const rsrc_t rx = make_rsrc(xb + (int64_t)t0 * a.xp, (int)(((rows - 1) * a.xp + vw) * sizeof(T)));
-            if (i < rows) {
-                const T *p = xb + (int64_t)(t0 + i) * a.xp;
-#pragma unroll
-                for (int vt = 0; vt < 4; ++vt)
-                    if (16 * vt + 4 * g4 < vw) {
-                        const f32x4 x = load4(p + 16 * vt + 4 * g4);
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) part += o[vt][r] * x[r];
-                    }
-            }
-            if constexpr (KIND == kDq)
-#pragma unroll
-                for (int kk = 0; kk < BK; ++kk) {
-                    const int col = Tile<T>::kKeys * kk + Tile<T>::kStepKeys * g4;
-                    xf[kk] = __builtin_bit_cast(Key, buf_load_b128(rx, col < vw
-                        ? (uint32_t)((i * (int)a.xp + col) * (int)sizeof(T)) : ~0u));
+                for (int vt = 0; vt < 4; ++vt) {
+                    const Key s = *reinterpret_cast<const Key *>(
+                        sS + (16 * vt + c16) * SP + Tile<T>::kKeys * kk + Tile<T>::kStepKeys * g4);
+                    o[vt] = mma16(s, q[kk], o[vt]);
                 }
-        }
-
-        // scores, two tiles of 16 sources at a time, and what the chunk's own tokens give
-        const float hi_i = sHi[i], lo_i = sLo[i];
+            const float in = sIn[i];
 #pragma unroll
-        for (int pr = 0; pr < 2; ++pr) {
-            if (REV ? 2 * pr + 1 < wave : 2 * pr > wave) {
+            for (int vt = 0; vt < 4; ++vt) o[vt] *= in;
+
+            // partner rows of the gradient of the decays
+            float part = 0.0f;
+            Key xf[KIND == kDq ? BK : 1];
+            if constexpr (KIND == kDq || KIND == kDk) {
+                const rsrc_t rx = make_rsrc(xb + (int64_t)t0 * a.xp, (int)(((rows - 1) * a.xp + vw) * sizeof(T)));
+                if (i < rows) {
+                    const T *p = xb + (int64_t)(t0 + i) * a.xp;
+#pragma unroll
+                    for (int vt = 0; vt < 4; ++vt)
+                        if (16 * vt + 4 * g4 < vw) {
+                            const f32x4 x = load4(p + 16 * vt + 4 * g4);
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) part += o[vt][r] * x[r];
+                        }
+                }
                 if constexpr (KIND == kDq)
-                    if (c16 == 15)
-#pragma unroll
-                        for (int r = 0; r < 8; ++r) sC[wave][32 * pr + 16 * (r >> 2) + 4 * g4 + (r & 3)] = 0.0f;
-                continue;
-            }
-            f32x4 p[2];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int s0 = 32 * pr + 16 * u;
-                p[u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int kk = 0; kk < KK; ++kk) {
-                    const Key k = *reinterpret_cast<const Key *>(
-                        sK + (s0 + c16) * KP + Tile<T>::kKeys * kk + Tile<T>::kStepKeys * g4);
-                    p[u] = mma16(k, q[kk], p[u]);
-                }
-                const f32x4 hs = load4(sHi + s0 + 4 * g4), ls = load4(sLo + s0 + 4 * g4);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int s = s0 + 4 * g4 + r;
-                    const float e = REV ? (hs[r] - hi_i) + (ls[r] - lo_i) : (hi_i - hs[r]) + (lo_i - ls[r]);
-                    p[u][r] = (REV ? s >= i : s <= i) ? p[u][r] * a.intra * fast_exp2(e) : 0.0f;
-                }
-                if constexpr (KIND == kDq) {
-                    // scores of the other pair: their products' sums by target and by source
-                    f32x4 m = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                     for (int kk = 0; kk < BK; ++kk) {
-                        const Key v = *reinterpret_cast<const Key *>(
-                            sV + (s0 + c16) * VP + Tile<T>::kKeys * kk + Tile<T>::kStepKeys * g4);
-                        m = mma16(v, xf[kk], m);
+                        const int col = Tile<T>::kKeys * kk + Tile<T>::kStepKeys * g4;
+                        xf[kk] = __builtin_bit_cast(Key, buf_load_b128(rx, col < vw
+                            ? (uint32_t)((i * (int)a.xp + col) * (int)sizeof(T)) : ~0u));
                     }
+            }
+
+            // scores, two tiles of 16 sources at a time, and what the chunk's own tokens give
+            const float hi_i = sHi[i], lo_i = sLo[i];
+#pragma unroll
+            for (int pr = 0; pr < 2; ++pr) {
+                if (REV ? 2 * pr + 1 < wave : 2 * pr > wave) {
+                    if constexpr (KIND == kDq)
+                        if (c16 == 15)
+#pragma unroll
+                            for (int r = 0; r < 8; ++r) sC[wave][32 * pr + 16 * (r >> 2) + 4 * g4 + (r & 3)] = 0.0f;
+                    continue;
+                }
+                f32x4 p[2];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int s0 = 32 * pr + 16 * u;
+                    p[u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int kk = 0; kk < KK; ++kk) {
+                        const Key k = *reinterpret_cast<const Key *>(
+                            sK + (s0 + c16) * KP + Tile<T>::kKeys * kk + Tile<T>::kStepKeys * g4);
+                        p[u] = mma16(k, q[kk], p[u]);
+                    }
+                    const f32x4 hs = load4(sHi + s0 + 4 * g4), ls = load4(sLo + s0 + 4 * g4);
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        const float prod = p[u][r] != 0.0f ? m[r] * p[u][r] : 0.0f;
-                        part += prod;
-                        const float col = columns_sum(prod);
-                        if (c16 == 15) sC[wave][s0 + 4 * g4 + r] = col;
+                        // selections before the exponential, which is formed for every pair: no
+                        // branches, and nothing not finite from a pair that does not count
+                        const int t = s0 + 4 * g4 + r;
+                        const bool keep = REV ? t >= i : t <= i;
+                        float e = REV ? (hs[r] - hi_i) + (ls[r] - lo_i) : (hi_i - hs[r]) + (lo_i - ls[r]);
+                        e = keep ? e : 0.0f;
+                        const float x = keep ? p[u][r] : 0.0f;
+                        p[u][r] = x * a.intra * fast_exp2(e);
+                    }
+                    if constexpr (KIND == kDq) {
+                        // scores of the other pair: their products' sums by target and by source
+                        f32x4 m = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                        for (int kk = 0; kk < BK; ++kk) {
+                            const Key v = *reinterpret_cast<const Key *>(
+                                sV + (s0 + c16) * VP + Tile<T>::kKeys * kk + Tile<T>::kStepKeys * g4);
+                            m = mma16(v, xf[kk], m);
+                        }
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const float prod = p[u][r] != 0.0f ? m[r] * p[u][r] : 0.0f;
+                            part += prod;
+                            const float col = columns_sum(prod);
+                            if (c16 == 15) sC[wave][s0 + 4 * g4 + r] = col;
+                        }
                     }
                 }
-            }
-            const Src ps = pack_src<T>(p[0], p[1]);
+                const Src ps = pack_src<T>(p[0], p[1]);
 #pragma unroll
-            for (int vt = 0; vt < 4; ++vt)
-                o[vt] = mma16(load_src(sV, VP, 32 * pr, 16 * vt, lane), ps, o[vt]);
-        }
-        if constexpr (KIND != kOut) {
-            part = rows_sum(part);
-            if (KIND == kDq && g4 == 0) sZ[i] = part;
-            if (KIND == kDk && g4 == 0 && i < rows) a.part[(bh * a.nvb + vb) * a.L + t0 + i] = part;
-        }
-        if (i < rows) {
-            const int64_t at = ((row0 + t0 + i) * a.H + h) * a.vd + v0;
-#pragma unroll
-            for (int vt = 0; vt < 4; ++vt) {
-                const int v = 16 * vt + 4 * g4;
-                if (v < vw) {
-                    if (a.o32) store4((float *)a.o + at + v, o[vt]);
-                    else store4((T *)a.o + at + v, o[vt]);
-                }
+                for (int vt = 0; vt < 4; ++vt)
+                    o[vt] = mma16(load_src(sV, VP, 32 * pr, 16 * vt, lane), ps, o[vt]);
             }
-        }
+            if constexpr (KIND == kDq || KIND == kDk) {
+                part = rows_sum(part);
+                if (KIND == kDq && g4 == 0) sZ[i] = part;
+                if (KIND == kDk && g4 == 0 && i < rows) a.part[(bh * a.nvb + vb) * a.L + t0 + i] = part;
+            }
+            if (a.o32) store_out((float *)a.o, t0, rows, i, o);
+            else store_out((T *)a.o, t0, rows, i, o);
 
-        if constexpr (KIND != kOut) {
-            // states before the chunk out of the forward walk; their products with the gradients
-            // of the states behind it in the backward one
-            float x = 0.0f;
-            T *sc = (T *)a.states + ((bh * a.nchunks + c) * a.vd + v0 + val) * a.kd;
+            if constexpr (KIND == kDq || KIND == kDk) {
+                // states before the chunk out of the forward walk; their products with the gradients
+                // of the states behind it in the backward one
+                float x = 0.0f;
+                T *sc = (T *)a.states + ((bh * a.nchunks + c) * a.vd + v0 + val) * a.kd;
 #pragma unroll
-            for (int kt = 0; kt < KT; ++kt) {
-                const int key = 16 * kt + 4 * g4;
-                if (has_val && key < a.kd) {
-                    if (KIND == kDq) {
-                        store4(sc + key, S[kt]);
-                    } else {
-                        const f32x4 s = load4(sc + key);
+                for (int kt = 0; kt < KT; ++kt) {
+                    const int key = 16 * kt + 4 * g4;
+                    if (has_val && key < a.kd) {
+                        if (KIND == kDq) {
+                            store4(sc + key, S[kt]);
+                        } else {
+                            const f32x4 s = load4(sc + key);
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) x += s[r] * S[kt][r];
+                            for (int r = 0; r < 4; ++r) x += s[r] * S[kt][r];
+                        }
                     }
                 }
-            }
-            if constexpr (KIND == kDk) {
-                x = rows_sum(columns_sum(x)) * whole;
-                if (lane == 15) sX[wave] = x;
+                if constexpr (KIND == kDk) {
+                    x = rows_sum(columns_sum(x)) * whole;
+                    if (lane == 15) sX[wave] = x;
+                }
             }
         }
 
@@ -488,11 +538,16 @@ __global__ __launch_bounds__(kThreads, DK * sizeof(T) <= 256 ? 2 : 1) void walk_
             } else {
                 bf16x8 wv[3];
                 split3(v, w, wv);
+                // four tiles side by side: a product's three parts wait for each other
 #pragma unroll
-                for (int kt = 0; kt < KT; ++kt) {
-                    const Src k = load_src(sK, KP, 32 * pr, 16 * kt, lane);
+                for (int kt = 0; kt < KT; kt += 4) {
+                    Src k[4];
 #pragma unroll
-                    for (int e = 0; e < 3; ++e) S[kt] = mma16(k, wv[e], S[kt]);
+                    for (int i = 0; i < 4; ++i) k[i] = load_src(sK, KP, 32 * pr, 16 * (kt + i), lane);
+#pragma unroll
+                    for (int e = 0; e < 3; ++e)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) S[kt + i] = mma16(k[i], wv[e], S[kt + i]);
                 }
             }
         }
@@ -504,12 +559,56 @@ __global__ __launch_bounds__(kThreads, DK * sizeof(T) <= 256 ? 2 : 1) void walk_
             a.cross[(bh * a.nvb + vb) * a.nchunks + c] = ((sX[0] + sX[1]) + sX[2]) + sX[3];
     }
 
-    if (a.last && has_val) {
-        float *p = a.last + bh * a.kd * a.vd + (int64_t)(v0 + val) * a.kd;
+    if constexpr (KIND == kEnds) {
+        if (tid == 0 && vb == 0) a.decays[bh * a.nseg + s] = passed;
+        if (has_val) {
+            float *p = a.ends + (bh * a.nseg + s + 1) * size + (int64_t)(v0 + val) * a.sv;
+#pragma unroll
+            for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int key = 16 * kt + 4 * g4 + r;
+                    if (key < a.kd) p[key * a.sk] = S[kt][r];
+                }
+        }
+    } else if (a.last && has_val && s == a.nseg - 1) {
+        float *p = a.last + bh * size + (int64_t)(v0 + val) * a.kd;
 #pragma unroll
         for (int kt = 0; kt < KT; ++kt)
             if (16 * kt + 4 * g4 < a.kd)
                 store4(p + 16 * kt + 4 * g4, S[kt]);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Starts of the segments of every head out of their ends, in place: a thread for four elements of a
+// head's state, eight segments' ends on their way at a time.
+// ---------------------------------------------------------------------------
+__global__ __launch_bounds__(kThreads) void chain_kernel(float *ends, const float *__restrict__ decays,
+                                                         const float *__restrict__ init, int64_t quads,
+                                                         int size4, int nseg)
+{
+    constexpr int kAhead = 8;
+    const int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    if (id >= quads) return;
+    const int64_t bh = id / size4;
+    f32x4 *p = reinterpret_cast<f32x4 *>(ends) + bh * nseg * size4 + id % size4;
+    f32x4 S = init ? reinterpret_cast<const f32x4 *>(init)[id] : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int s0 = 0; s0 < nseg; s0 += kAhead) {
+        f32x4 end[kAhead];
+        float d[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int s = min(s0 + i, nseg - 2);
+            end[i] = p[(int64_t)(s + 1) * size4];
+            d[i] = decays[bh * nseg + s];
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            if (s0 + i >= nseg) break;
+            p[(int64_t)(s0 + i) * size4] = S;
+            S = S * d[i] + end[i];
+        }
     }
 }
 
@@ -584,10 +683,11 @@ unsigned groups_for(int64_t work, int each)
 }
 
 template <typename T, int DK, bool REV, Kind KIND>
-hipError_t walk_go(const Walk &a, int64_t bh, hipStream_t st)
+hipError_t walk_go(Walk a, int64_t bh, hipStream_t st)
 {
-    hipLaunchKernelGGL((walk_kernel<T, DK, REV, KIND>), dim3((unsigned)(bh * a.nvb)), dim3(kThreads), 0,
-                       st, a);
+    a.groups = bh * (KIND == kEnds ? a.nseg - 1 : a.nseg);
+    const int64_t blocks = (a.groups + 7) / 8 * 8 * a.nvb;
+    hipLaunchKernelGGL((walk_kernel<T, DK, REV, KIND>), dim3((unsigned)blocks), dim3(kThreads), 0, st, a);
     return hipGetLastError();
 }
 
@@ -599,14 +699,60 @@ hipError_t walk_by_key(const Walk &a, int64_t bh, hipStream_t st)
     return walk_go<T, 256, REV, KIND>(a, bh, st);
 }
 
+// The ends of a walk's segments, and their starts.
+template <typename T, bool REV> hipError_t starts_go(const Walk &a, int64_t bh, hipStream_t st)
+{
+    const hipError_t e = walk_by_key<T, REV, kEnds>(a, bh, st);
+    if (e != hipSuccess) return e;
+    const int size4 = a.kd * a.vd / 4;
+    const int64_t quads = bh * size4;
+    hipLaunchKernelGGL(chain_kernel, dim3((unsigned)((quads + kThreads - 1) / kThreads)), dim3(kThreads), 0,
+                       st, a.ends, a.decays, a.init, quads, size4, a.nseg);
+    return hipGetLastError();
+}
+
 int blocks_of(int64_t values) { return (int)((values + kBlock - 1) / kBlock); }
 
+// How the chunks of a walk are split into segments, whose ends a first walk leaves.
+struct Split {
+    int seg, nseg;
+};
+Split split_of(int64_t walks, int chunks)
+{
+    constexpr int kWant = 512, kLeast = 4;
+    const int64_t n = (kWant + walks - 1) / walks;
+    int seg = (int)((chunks + n - 1) / n);
+    if (seg < kLeast) seg = kLeast;
+    return {seg, (chunks + seg - 1) / seg};
+}
+
 int chunks_of(const LinattnShape &s) { return (int)((s.L + kChunk - 1) / kChunk); }
+
+// Workspace of one split: ends and decays (byte offsets).
+int64_t ends_bytes(const LinattnShape &s, int nseg)
+{
+    return nseg > 1 ? s.b * s.H * nseg * s.dk * s.dv * 4 : 0;
+}
+int64_t decays_bytes(const LinattnShape &s, int nseg)
+{
+    return nseg > 1 ? (s.b * s.H * nseg * 4 + 255) / 256 * 256 : 0;
+}
+Split forward_split(const LinattnShape &s)
+{
+    return split_of(s.b * s.H * blocks_of(s.dv), chunks_of(s));
+}
+
+Split grad_split(const LinattnShape &s)
+{
+    const int64_t least = blocks_of(s.dk) < blocks_of(s.dv) ? blocks_of(s.dk) : blocks_of(s.dv);
+    return split_of(s.b * s.H * least, chunks_of(s));
+}
 
 // Workspace of the gradients (byte offsets, on 256 bytes): with a decays' gradient the states
 // before each chunk and the parts that its kernel adds up; with shared heads every head's dq and dk.
 struct GradLayout {
-    int64_t states, read, written, cross, dq, dk, bytes;
+    int64_t states, read, written, cross, dq, dk, ends, decays, back_ends, back_decays, bytes;
+    Split split;
 };
 GradLayout grad_layout(const LinattnShape &s, bool gates)
 {
@@ -625,6 +771,12 @@ GradLayout grad_layout(const LinattnShape &s, bool gates)
     const int64_t heads = s.b * s.L * s.H * s.dk * 4;
     y.dq = take(s.H > s.G, heads);
     y.dk = take(s.H > s.G, heads);
+    y.split = grad_split(s);
+    const int nseg = y.split.nseg;
+    y.ends = take(nseg > 1, ends_bytes(s, nseg));
+    y.decays = take(nseg > 1, decays_bytes(s, nseg));
+    y.back_ends = take(nseg > 1, ends_bytes(s, nseg));
+    y.back_decays = take(nseg > 1, decays_bytes(s, nseg));
     y.bytes = at;
     return y;
 }
@@ -642,6 +794,14 @@ template <typename T> hipError_t forward_go(const LinattnShape &s, const Linattn
     w.inter = w.intra = s.scale;
     w.L = (int)s.L; w.H = (int)s.H; w.kd = (int)s.dk; w.vd = (int)s.dv;
     w.nvb = blocks_of(s.dv);
+    const Split y = forward_split(s);
+    w.seg = y.seg; w.nseg = y.nseg;
+    w.ends = (float *)a.ws;
+    w.decays = (float *)((char *)a.ws + ends_bytes(s, y.nseg));
+    if (y.nseg > 1) {
+        const hipError_t e = starts_go<T, false>(w, s.b * s.H, st);
+        if (e != hipSuccess) return e;
+    }
     return walk_by_key<T, false, kOut>(w, s.b * s.H, st);
 }
 
@@ -665,6 +825,28 @@ hipError_t backward_go(const LinattnShape &s, const LinattnGradArgs &a, hipStrea
     w.states = at(y.states);
     w.cross = (float *)at(y.cross);
 
+    w.seg = y.split.seg; w.nseg = y.split.nseg;
+    Walk back = w;       // states' gradients, back in time
+    w.ends = (float *)at(y.ends); w.decays = (float *)at(y.decays);
+    back.ends = (float *)at(y.back_ends); back.decays = (float *)at(y.back_decays);
+    if (w.nseg > 1) {
+        Walk f = w, r = back;
+        f.k = a.k; f.kp = s.kp; f.kdiv = share;
+        f.v = a.v; f.vp = s.vp; f.vdiv = 1;
+        f.init = a.h0; f.weight = 1.0f;
+        r.k = a.q; r.kp = s.qp; r.kdiv = share;
+        r.v = a.dout; r.vp = s.dop; r.vdiv = 1;
+        r.init = a.dhT; r.weight = s.scale;
+        for (Walk *x : {&f, &r}) {
+            x->qdiv = 1;
+            x->sv = s.dk; x->sk = 1;
+            x->kd = (int)s.dk; x->vd = (int)s.dv; x->nvb = blocks_of(s.dv);
+        }
+        e = starts_go<T, false>(f, bh, st);
+        if (e == hipSuccess) e = starts_go<T, true>(r, bh, st);
+        if (e != hipSuccess) return e;
+    }
+
     Walk q = w;          // dq = scale S^T do
     q.q = a.dout; q.qp = s.dop; q.qdiv = 1;
     q.k = a.v; q.kp = s.vp; q.kdiv = 1;
@@ -678,7 +860,7 @@ hipError_t backward_go(const LinattnShape &s, const LinattnGradArgs &a, hipStrea
     e = gates ? walk_by_key<T, false, kDq>(q, bh, st) : walk_by_key<T, false, kOut>(q, bh, st);
     if (e != hipSuccess) return e;
 
-    Walk k = w;          // dk = dS^T v, scale in dS
+    Walk k = back;       // dk = dS^T v, scale in dS
     k.q = a.v; k.qp = s.vp; k.qdiv = 1;
     k.k = a.dout; k.kp = s.dop; k.kdiv = 1;
     k.v = a.q; k.vp = s.qp; k.vdiv = share;
@@ -691,7 +873,7 @@ hipError_t backward_go(const LinattnShape &s, const LinattnGradArgs &a, hipStrea
     e = gates ? walk_by_key<T, true, kDk>(k, bh, st) : walk_by_key<T, true, kOut>(k, bh, st);
     if (e != hipSuccess) return e;
 
-    Walk v = w;          // dv = dS k
+    Walk v = back;       // dv = dS k
     v.q = a.k; v.qp = s.kp; v.qdiv = share;
     v.k = a.q; v.kp = s.qp; v.kdiv = share;
     v.v = a.dout; v.vp = s.dop; v.vdiv = 1;
@@ -731,6 +913,12 @@ hipError_t backward_go(const LinattnShape &s, const LinattnGradArgs &a, hipStrea
 hipError_t launch_linattn(const LinattnShape &s, const LinattnArgs &a, hipStream_t st)
 {
     return s.bf16 ? forward_go<bf16>(s, a, st) : forward_go<float>(s, a, st);
+}
+
+size_t linattn_workspace_bytes(const LinattnShape &s)
+{
+    const int n = forward_split(s).nseg;
+    return n > 1 ? (size_t)(ends_bytes(s, n) + decays_bytes(s, n)) : SSD_LINATTN_NO_WORKSPACE;
 }
 
 size_t linattn_backward_workspace_bytes(const LinattnShape &s)

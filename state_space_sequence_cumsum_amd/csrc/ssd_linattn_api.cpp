@@ -110,7 +110,7 @@ ssd_status ssd_linattn_validate(const ssd_linattn_problem *problem) { return che
 
 size_t ssd_linattn_workspace_bytes(const ssd_linattn_problem *problem)
 {
-    return check_linattn(problem) == SSD_OK ? SSD_LINATTN_NO_WORKSPACE : 0;
+    return check_linattn(problem) == SSD_OK ? ssd::linattn_workspace_bytes(linattn_shape(problem)) : 0;
 }
 
 ssd_status ssd_linattn(const ssd_linattn_problem *problem, const void *q, const void *k,
