@@ -27,6 +27,8 @@
 // that states, which leave the kernel in fp32, hold fp32's precision.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+
 #include "../../include/ssd.h"
 #include "ssd_device.h"
 #include "ssd_launch.h"
@@ -34,8 +36,10 @@
 namespace ssd {
 namespace {
 
-constexpr int kChunk = 64;       // tokens of a chunk
-constexpr int kBlock = 64;       // values of a walk
+// Tokens of a chunk: 64, or 32 of the widest fp32 heads, whose rows would not fit into LDS and
+// registers otherwise.
+template <typename T, int DK> constexpr int chunk_tokens() { return DK * sizeof(T) <= 512 ? 64 : 32; }
+int chunk_tokens(bool bf16, int64_t keys) { return bf16 || keys <= 128 ? 64 : 32; }
 constexpr int kThreads = 256;    // four waves
 
 // What a walk is run for: the state that a segment of chunks leaves, from zero; an output (of the
@@ -55,23 +59,23 @@ struct Walk {
     bool o32;                   // in fp32 (else in the inputs' type)
     const float *init;          // value v, key k of a head at v sv + k sk; may be NULL
     int64_t sv, sk;
-    float *last;                // [b, H, vd, kd]; may be NULL
-    // Segments: `seg` chunks each, nseg of them, in the walk's order.  With more than one, kEnds
+    float *last;                // [b, H, vd, kd], of a walk of one segment; may be NULL
+    // Segments: `seg` tokens each (a multiple of 64), nseg of them, in the walk's order.  With more than one, kEnds
     // leaves their ends (from zero) and decays, a chain over those their starts, for the others.
     int seg, nseg;
-    float *ends;                // [b H, nseg, vd kd] in init's layout: segment s's end at s + 1, then
-                                // its start at s
+    float *ends;                // [b H, nseg, vd kd], in init's layout: ends, then starts
     float *decays;              // [b H, nseg]: over segment s
     float inter, intra;         // factors of an output's two parts
     float weight;               // factor of what is added to the state
     int L, H, kd, vd, nvb;
     int64_t groups;             // heads x segments
-    // kDq, kDk: the array whose product with the output the decays' gradient takes (q, k), this
-    // walk's part of it, and the states before each chunk, [b H, chunks, vd, kd]
+    // kDq, kDk: the array whose products with the outputs the decays' gradient takes (q, k): those
+    // (kDk: of what the chunk's own tokens give, and of what the state behind it gives), and the states
+    // before each chunk, [b H, chunks, vd, kd], with their products with the gradients behind it
     const void *x;
     int64_t xp;
     int xdiv;
-    float *part;                // [b H, nvb, L]
+    float *part, *written;      // [b H, nvb, L]
     void *states;
     float *cross;               // [b H, nvb, chunks]
     int nchunks;
@@ -81,36 +85,31 @@ struct DecayGradient {
     const void *g;
     int64_t gp;
     const int32_t *lengths;
-    const float *read, *written, *cross;
+    const float *read, *own, *written, *cross;
     void *dg;
     int64_t bh;
-    int L, H, nvb, nchunks;
+    int L, H, nvb, nchunks, chunk;
 };
 
 // ---------------------------------------------------------------------------
-// Tiles of 16 x 16.  An accumulator's lane l holds column l % 16, rows 4 (l / 16) + r.
-// A key fragment is 16 bytes of a row (row l % 16): bf16 keys 8 (l / 16) + e of 32, one
-// instruction; fp32 keys 4 (l / 16) + e of 16, one instruction for each e.  A source fragment
-// is eight tokens of one column (column l % 16), in the order in which two accumulators
-// hold their rows: tokens 4 (l / 16) + e of the first 16 and of the second.
+// Tiles of 16 x 16.  An accumulator's lane l holds column l % 16, rows 4 (l / 16) + r.  An operand's
+// fragment holds 16 bytes of one row (A) or column (B), l % 16, along the contracted index: a step
+// of it, 32 for bf16 (one instruction) or 16 for fp32 (one for each of the four).  There are two
+// orders, the same for both operands of a product:
+//   straight  bf16 8 (l / 16) + e, fp32 4 (l / 16) + e: what a 16-byte read of a row gives
+//   paired    bf16 4 (l / 16) + e and 16 + 4 (l / 16) + e, fp32 as straight: what two accumulators
+//             (fp32: one), one behind the other along the rows, hold as they stand
 // ---------------------------------------------------------------------------
 template <typename T> struct Tile;
 template <> struct Tile<bf16> {
-    typedef bf16x8 key;
-    typedef bf16x8 src;
-    static constexpr int kKeys = 32;
-    static constexpr int kStepKeys = 8;
-    // 32 bytes off a multiple of 128: the transpose reads' four rows in different banks
-    static constexpr int pitch(int n) { return n + 16; }
-    static constexpr int state_pitch(int n) { return n + 8; }
+    typedef bf16x8 frag;
+    static constexpr int kStep = 32, kPart = 8;
+    static constexpr int row_pitch(int n) { return n + 8; }
 };
 template <> struct Tile<float> {
-    typedef f32x4 key;
-    typedef f32x8 src;
-    static constexpr int kKeys = 16;
-    static constexpr int kStepKeys = 4;
-    static constexpr int pitch(int n) { return n + 4; }
-    static constexpr int state_pitch(int n) { return n + 4; }
+    typedef f32x4 frag;
+    static constexpr int kStep = 16, kPart = 4;
+    static constexpr int row_pitch(int n) { return n + 4; }
 };
 
 __device__ __forceinline__ f32x4 mma16(const bf16x8 &a, const bf16x8 &b, f32x4 c)
@@ -123,92 +122,171 @@ __device__ __forceinline__ f32x4 mma16(const f32x4 &a, const f32x4 &b, f32x4 c)
     for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[e], c, 0, 0, 0);
     return c;
 }
-__device__ __forceinline__ f32x4 mma16(const f32x8 &a, const f32x8 &b, f32x4 c)
-{
-#pragma unroll
-    for (int e = 0; e < 8; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[e], c, 0, 0, 0);
-    return c;
-}
 
-// The source fragment of tokens `row` .. `row` + 31 and columns `col` .. `col` + 15 of a tile
-// stored token by token.
-__device__ __forceinline__ bf16x8 load_src(const bf16 *s, int pitch, int row, int col, int lane)
-{
-    const bf16 *p = s + (row + 4 * (lane >> 4) + ((lane & 15) >> 2)) * pitch + col + 4 * (lane & 3);
-    return cat8(tr_read4(p), tr_read4(p + 16 * pitch));
-}
-__device__ __forceinline__ f32x8 load_src(const float *s, int pitch, int row, int col, int lane)
-{
-    const float *p = s + (row + 4 * (lane >> 4)) * pitch + col + (lane & 15);
-    f32x8 f;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) { f[e] = p[e * pitch]; f[4 + e] = p[(16 + e) * pitch]; }
-    return f;
-}
+// ---------------------------------------------------------------------------
+// Rows of queries and keys in LDS, N elements each.  For bf16 a row's pieces of 16 bytes change
+// places by the row (exclusive or with bits of it): the 16 rows of a fragment's straight read, the
+// 8 rows of half a transpose read (two pieces of each) and the rows of a paired read then all lie
+// in different banks, which no padding gives (at 288 bytes a row straight reads of 16 rows
+// conflicted, at 272 transpose reads of 8).  fp32 rows are padded by 16 bytes.
+// ---------------------------------------------------------------------------
+// A lane's place is one offset; what a fragment's step and tile add to it is a constant, `on` (an
+// exclusive or of bits that the lane's own columns leave free, or a sum).
+template <typename T, int N> struct Rows;
+template <int N> struct Rows<bf16, N> {
+    // 16 rows and 16 bytes: halves of two tiles' fragments that lie a multiple of 512 bytes apart
+    // would be read by one instruction, and then moved (57 moves a chunk of 128 values)
+    static constexpr int kTile = 16 * N + 8;
+    // elements from the start of the rows to row r's piece of column c (a multiple of 8)
+    static __device__ __forceinline__ int at(int r, int c)
+    {
+        const int turn = N == 64 ? (r >> 1 & 3) << 1 | (r >> 3 & 1) : (r & 7) << 1 | (r >> 3 & 1);
+        return r * N + (r >> 4) * 8 + ((c >> 3) ^ turn) * 8;
+    }
+    static __device__ __forceinline__ int on(int off, int columns) { return off ^ columns; }
+    // places of a lane in row l % 16 of straight and paired fragments, and down 16 columns
+    static __device__ __forceinline__ int straight(int lane) { return at(lane & 15, 8 * (lane >> 4)); }
+    static __device__ __forceinline__ int paired(int lane)
+    {
+        return at(lane & 15, 8 * (lane >> 5)) + 4 * (lane >> 4 & 1);
+    }
+    static __device__ __forceinline__ int down(int lane)
+    {
+        return at(4 * (lane >> 4) + ((lane & 15) >> 2), 8 * (lane >> 1 & 1)) + 4 * (lane & 1);
+    }
+};
+template <int N> struct Rows<float, N> {
+    static constexpr int kPitch = N + 4, kTile = 16 * kPitch;
+    static __device__ __forceinline__ int at(int r, int c) { return r * kPitch + c; }
+    static __device__ __forceinline__ int on(int off, int columns) { return off + columns; }
+    static __device__ __forceinline__ int straight(int lane) { return at(lane & 15, 4 * (lane >> 4)); }
+    static __device__ __forceinline__ int paired(int lane) { return straight(lane); }
+    static __device__ __forceinline__ int down(int lane) { return at(4 * (lane >> 4), lane & 15); }
+};
 
-// acc += a (w x)^T for the source fragments a and x: three bf16 parts of each product w x
-// hold its 24 bits.
-__device__ __forceinline__ void split3(const bf16x8 &x, const f32x8 &w, bf16x8 (&p)[3])
+// A straight or paired fragment of step m of row 16 i + l % 16.
+template <int N, typename T>
+__device__ __forceinline__ typename Tile<T>::frag load_straight(const T *s, int place, int i, int m)
 {
+    typedef Rows<T, N> R;
+    return *reinterpret_cast<const typename Tile<T>::frag *>(s + i * R::kTile +
+                                                             R::on(place, Tile<T>::kStep * m));
+}
+template <int N> __device__ __forceinline__ bf16x8 load_paired(const bf16 *s, int place, int i, int m)
+{
+    const bf16 *p = s + i * Rows<bf16, N>::kTile;
+    return cat8(*reinterpret_cast<const bf16x4 *>(p + (place ^ 32 * m)),
+                *reinterpret_cast<const bf16x4 *>(p + (place ^ (32 * m + 16))));
+}
+template <int N> __device__ __forceinline__ f32x4 load_paired(const float *s, int place, int i, int m)
+{
+    return load_straight<N>(s, place, i, m);
+}
+// A paired fragment of step m of rows, down columns 16 j + l % 16.
+template <int N> __device__ __forceinline__ bf16x8 load_down(const bf16 *s, int place, int m, int j)
+{
+    constexpr int tile = Rows<bf16, N>::kTile;
+    const bf16 *p = s + 2 * m * tile + (place ^ 16 * j);
+    return cat8(tr_read4(p), tr_read4(p + tile));
+}
+template <int N> __device__ __forceinline__ f32x4 load_down(const float *s, int place, int m, int j)
+{
+    constexpr int pitch = Rows<float, N>::kPitch;
+    const float *p = s + 16 * m * pitch + place + 16 * j;
+    return f32x4{p[0], p[pitch], p[2 * pitch], p[3 * pitch]};
+}
+// A paired fragment of step m out of accumulators.
+template <typename T, int N>
+__device__ __forceinline__ typename Tile<T>::frag of_accumulators(const f32x4 (&acc)[N], int m)
+{
+    if constexpr (sizeof(T) == 4) {
+        return acc[m];
+    } else {
+        u32x4 r;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        float v = (float)x[e] * w[e];
-#pragma unroll
-        for (int i = 0; i < 3; ++i) {
-            p[i][e] = (bf16)v;
-            v -= (float)p[i][e];
+        for (int i = 0; i < 2; ++i) {
+            r[2 * i] = pack_bf16(acc[2 * m + i][0], acc[2 * m + i][1]);
+            r[2 * i + 1] = pack_bf16(acc[2 * m + i][2], acc[2 * m + i][3]);
         }
+        return __builtin_bit_cast(bf16x8, r);
     }
 }
-
-template <typename T> __device__ __forceinline__ typename Tile<T>::src pack_src(const f32x4 &a,
-                                                                                 const f32x4 &b);
-template <> __device__ __forceinline__ bf16x8 pack_src<bf16>(const f32x4 &a, const f32x4 &b)
+// Where source `s` of a target's scores is kept, for a paired read of 16 bytes.
+template <typename T> __device__ __forceinline__ int paired_place(int tile, int g4)
 {
-    bf16x8 r;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) { r[e] = (bf16)a[e]; r[4 + e] = (bf16)b[e]; }
-    return r;
+    if constexpr (sizeof(T) == 4) return 16 * tile + 4 * g4;
+    else return 32 * (tile >> 1) + 8 * g4 + 4 * (tile & 1);
 }
-template <> __device__ __forceinline__ f32x8 pack_src<float>(const f32x4 &a, const f32x4 &b)
+
+// The products w x of a fragment and its tokens' weights as operands: three bf16 parts hold a
+// product's 24 bits (two 16 of them), fp32 is one.
+template <int PARTS>
+__device__ __forceinline__ void weigh(const bf16x8 &x, const float *w, int m, int g4, bf16x8 (&p)[PARTS])
 {
-    f32x8 r;
+    const f32x4 w0 = *reinterpret_cast<const f32x4 *>(w + 32 * m + 4 * g4);
+    const f32x4 w1 = *reinterpret_cast<const f32x4 *>(w + 32 * m + 16 + 4 * g4);
+    f32x8 v;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) { r[e] = a[e]; r[4 + e] = b[e]; }
-    return r;
+    for (int e = 0; e < 4; ++e) { v[e] = (float)x[e] * w0[e]; v[4 + e] = (float)x[4 + e] * w1[e]; }
+#pragma unroll
+    for (int i = 0; i < PARTS; ++i) {
+        u32x4 r;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            r[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
+            v[2 * e] -= bf_lo(r[e]);
+            v[2 * e + 1] -= bf_hi(r[e]);
+        }
+        p[i] = __builtin_bit_cast(bf16x8, r);
+    }
+}
+template <int PARTS>
+__device__ __forceinline__ void weigh(const f32x4 &x, const float *w, int m, int g4, f32x4 (&p)[PARTS])
+{
+    p[0] = x * *reinterpret_cast<const f32x4 *>(w + 16 * m + 4 * g4);
 }
 
 // Four elements as T, in LDS or memory.
 __device__ __forceinline__ void store4(bf16 *p, const f32x4 &v)
 {
-    bf16x4 r;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) r[e] = (bf16)v[e];
-    *reinterpret_cast<bf16x4 *>(p) = r;
+    u32x2 r;
+    r[0] = pack_bf16(v[0], v[1]);
+    r[1] = pack_bf16(v[2], v[3]);
+    *reinterpret_cast<u32x2 *>(p) = r;
 }
 __device__ __forceinline__ void store4(float *p, const f32x4 &v) { *reinterpret_cast<f32x4 *>(p) = v; }
-__device__ __forceinline__ f32x4 load4(const bf16 *p)
-{
-    const bf16x4 v = *reinterpret_cast<const bf16x4 *>(p);
-    f32x4 r;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) r[e] = (float)v[e];
-    return r;
-}
 __device__ __forceinline__ f32x4 load4(const float *p) { return *reinterpret_cast<const f32x4 *>(p); }
 
-// The same through a buffer, past whose end nothing is written.
+// The same through a buffer: past its end nothing is written, and zeros are read.
+typedef unsigned int u2 __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ void buf_store4(rsrc_t r, uint32_t off, const f32x4 &v, bf16 *)
 {
-    u32x2 w;
+    u2 w;
     w[0] = pack_bf16(v[0], v[1]);
     w[1] = pack_bf16(v[2], v[3]);
-    __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(__attribute__((ext_vector_type(2))) unsigned int, w), r,
-                                          (int)off, 0, 0);
+    __builtin_amdgcn_raw_buffer_store_b64(w, r, (int)off, 0, 0);
 }
 __device__ __forceinline__ void buf_store4(rsrc_t r, uint32_t off, const f32x4 &v, float *)
 {
     buf_store_b128(r, off, __builtin_bit_cast(u32x4, v));
+}
+// Four elements as they come, and as fp32.
+template <typename T> struct Raw4;
+template <> struct Raw4<bf16> { typedef u2 t; };
+template <> struct Raw4<float> { typedef u32x4 t; };
+__device__ __forceinline__ u2 buf_load4(rsrc_t r, uint32_t off, bf16 *)
+{
+    return __builtin_amdgcn_raw_buffer_load_b64(r, (int)off, 0, 0);
+}
+__device__ __forceinline__ u32x4 buf_load4(rsrc_t r, uint32_t off, float *) { return buf_load_b128(r, off); }
+__device__ __forceinline__ f32x4 as_floats(const u2 &v)
+{
+    return f32x4{bf_lo(v[0]), bf_hi(v[0]), bf_lo(v[1]), bf_hi(v[1])};
+}
+__device__ __forceinline__ f32x4 as_floats(const u32x4 &v) { return __builtin_bit_cast(f32x4, v); }
+__device__ __forceinline__ float dot4(const f32x4 &a, const f32x4 &b)
+{
+    return fmaf(a[3], b[3], fmaf(a[2], b[2], fmaf(a[1], b[1], a[0] * b[0])));
 }
 
 // A token's log decay in base 2, between -1000 and 0; a NaN stays one.
@@ -233,32 +311,48 @@ __device__ __forceinline__ float columns_sum(float v)   // over the 16 lanes of 
 }
 
 // ---------------------------------------------------------------------------
-// A walk: one (batch, head) and 64 of its values, all chunks.
-//
-// Products per chunk and wave (w the wave, i its 16 targets, all transposed so that an
-// accumulator is the next product's operand as it stands):
-//   scores [source, i] = K q_i          keys contracted, K from LDS, q from memory
-//   o [value, i] = S q_i                S [value, key] rounded into LDS by the last chunk
-//   o += V^T scores                     tokens contracted, V read transposed
-//   S [key, value w] += K^T (w V)       tokens contracted, K read transposed
-// The next chunk's K, V and q are on their way while these run.
+// A walk: one (batch, head) and a block of 64 NV of its values, chunk by chunk.  Each of the four
+// waves has 16 NV values: their state [key, value], whose accumulators are an operand as they stand,
+// and their outputs [value, target].  A chunk's products, a wave's share:
+//   scores [source, target]   of the ten 16 x 16 tiles on this side of the diagonal, two or three;
+//                             decayed and rounded, they go to the other waves through LDS
+//   o = S q                   keys contracted, all targets
+//   S += K^T (w V)            tokens contracted, K and V read transposed
+//   o += V^T scores           tokens contracted, behind the second of the two barriers of a chunk
+// The next chunk's rows are on their way meanwhile, in registers.
 // ---------------------------------------------------------------------------
-template <typename T, int DK, bool REV, Kind KIND>
-__global__ __launch_bounds__(kThreads, DK * sizeof(T) <= 256 ? 2 : 1) void walk_kernel(Walk a)
+// Waves of a SIMD that the registers leave room for: those of the workgroups that LDS holds.
+template <typename T, int DK, int NV> constexpr int waves_for()
 {
-    typedef typename Tile<T>::key Key;
-    typedef typename Tile<T>::src Src;
-    constexpr int KP = Tile<T>::pitch(DK), VP = Tile<T>::pitch(kBlock), SP = Tile<T>::state_pitch(DK);
-    constexpr int KK = DK / Tile<T>::kKeys, KT = DK / 16;
+    if (sizeof(T) == 2) return DK > 128 ? 1 : DK == 128 || NV == 2 ? 2 : 3;
+    return DK == 128 ? 1 : 2;
+}
+
+// PARTS: bf16 parts of what is added to the state, 3, or 2 where the state only makes outputs.
+template <typename T, int DK, int NV, bool REV, Kind KIND, int PARTS>
+__global__ __launch_bounds__(kThreads, (waves_for<T, DK, NV>())) void walk_kernel(Walk a)
+{
+    typedef typename Tile<T>::frag Frag;
+    typedef typename Raw4<T>::t Raw;
+    constexpr bool kOuts = KIND != kEnds, kParts = KIND == kDq || KIND == kDk;
+    constexpr int CH = chunk_tokens<T, DK>(), NI = CH / 16, kTiles = NI * (NI + 1) / 2;
+    constexpr int BV = 64 * NV;                                      // values
+    typedef Rows<T, DK> KeyRows;
+    typedef Rows<T, BV> ValRows;
+    constexpr int PP = Tile<T>::row_pitch(CH);                       // a target's scores
+    constexpr int KK = DK / Tile<T>::kStep, KT = DK / 16, MM = CH / Tile<T>::kStep;
     constexpr int kVec = 16 / (int)sizeof(T);                        // elements of 16 bytes
-    constexpr int KI = kChunk * DK / kVec / kThreads;                // 16-byte pieces a thread
-    constexpr int VI = kChunk * kBlock / kVec / kThreads;
-    constexpr int BK = kBlock / Tile<T>::kKeys;                      // fragments of 64 values
-    __shared__ __attribute__((aligned(16))) T sK[kChunk * KP];
-    __shared__ __attribute__((aligned(16))) T sV[kChunk * VP];
-    __shared__ __attribute__((aligned(16))) T sS[kBlock * SP];
-    __shared__ __attribute__((aligned(16))) float sHi[kChunk], sLo[kChunk], sIn[kChunk], sW[kChunk];
-    __shared__ float sZ[kChunk], sC[4][kChunk], sX[4];
+    constexpr int KI = CH * DK / kVec / kThreads;                // 16-byte pieces a thread
+    constexpr int VI = CH * BV / kVec / kThreads;
+    constexpr int QI = kOuts ? KI : 1, kSide = 2;
+    constexpr int KR = kThreads / (DK / kVec), VR = kThreads / (BV / kVec);  // rows of a round of pieces
+    static_assert(KI * KR == CH && VI * VR == CH, "pieces of whole rows");
+    __shared__ __attribute__((aligned(16))) T sK[NI * KeyRows::kTile];
+    __shared__ __attribute__((aligned(16))) T sV[NI * ValRows::kTile];
+    __shared__ __attribute__((aligned(16))) T sQ[NI * KeyRows::kTile];
+    __shared__ __attribute__((aligned(16))) T sP[CH * PP];
+    __shared__ __attribute__((aligned(16))) float sHi[CH], sLo[CH], sIn[CH], sW[CH];
+    __shared__ float sPart[4][CH], sWritten[4][CH], sX[4];
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int c16 = lane & 15, g4 = lane >> 4;
@@ -266,326 +360,362 @@ __global__ __launch_bounds__(kThreads, DK * sizeof(T) <= 256 ? 2 : 1) void walk_
     // one, whose L2 then holds the q and k that they share
     const int64_t group = (int64_t)(blockIdx.x / (8 * a.nvb)) * 8 + blockIdx.x % 8;
     const int vb = blockIdx.x / 8 % a.nvb;
-    const int walks = KIND == kEnds ? a.nseg - 1 : a.nseg;
     if (group >= a.groups) return;
-    const int64_t bh = group / walks;
-    const int s = (int)(group % walks);
+    const int64_t bh = group / a.nseg;
+    const int s = (int)(group % a.nseg);
     const int64_t b = bh / a.H;
     const int h = (int)(bh % a.H);
-    const int v0 = vb * kBlock;
+    const int v0 = vb * BV;
     int n = a.L;
     if (a.lengths) n = min(max(a.lengths[b], 0), a.L);
-    const int nc = (n + kChunk - 1) / kChunk;
-    const int it0 = min(s * a.seg, nc), it1 = min(it0 + a.seg, nc);     // in the walk's order
+    // segment s in the walk's order: the s-th, or back in time the s-th from the sequence's end
+    const int nc = (n + CH - 1) / CH, seg = a.seg / CH;
+    const int at = REV ? (nc + seg - 1) / seg - 1 - s : s;
+    const int c0 = at < 0 ? 0 : min(at * seg, nc), count = at < 0 ? 0 : min(seg, nc - c0);
 
     const int64_t row0 = b * a.L;
     const T *qb = (const T *)a.q + row0 * a.qp + (int64_t)(h / a.qdiv) * a.kd;
     const T *kb = (const T *)a.k + row0 * a.kp + (int64_t)(h / a.kdiv) * a.kd;
     const T *vbp = (const T *)a.v + row0 * a.vp + (int64_t)(h / a.vdiv) * a.vd + v0;
-    const T *xb = KIND == kDq || KIND == kDk
-                      ? (const T *)a.x + row0 * a.xp + (int64_t)(h / a.xdiv) * a.vd + v0
-                      : nullptr;
-    const int vw = min(a.vd - v0, kBlock);
+    const T *xb = kParts ? (const T *)a.x + row0 * a.xp + (int64_t)(h / a.xdiv) * a.vd + v0 : nullptr;
+    const int vw = min(a.vd - v0, BV);
 
-    // the state's accumulators: column the wave's value, rows 16 keys each
-    const int val = 16 * wave + c16;
-    const bool has_val = val < vw;
+    // the state's accumulators: column a value, rows 16 keys each
+    const int val0 = 16 * NV * wave + c16, val4 = 16 * NV * wave + 4 * g4;   // and a target's four
     const int64_t size = (int64_t)a.kd * a.vd;
-    f32x4 S[KT];
+    f32x4 S[NV][KT];
+    const float *start = KIND == kEnds ? nullptr
+                         : a.nseg > 1  ? a.ends + (bh * a.nseg + s) * size
+                         : a.init      ? a.init + bh * size
+                                       : nullptr;
 #pragma unroll
-    for (int kt = 0; kt < KT; ++kt) {
-        S[kt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        const int key = 16 * kt + 4 * g4;
-        if (!has_val || key >= a.kd) continue;
-        const int64_t at = (int64_t)(v0 + val) * a.sv + (int64_t)key * a.sk;
-        const float *p = KIND == kEnds   ? nullptr
-                         : a.nseg > 1    ? a.ends + (bh * a.nseg + s) * size + at
-                         : a.init        ? a.init + bh * size + at
-                                         : nullptr;
-        if (p)
+    for (int v = 0; v < NV; ++v)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) S[kt][r] = p[r * a.sk];
-    }
+        for (int kt = 0; kt < KT; ++kt) {
+            S[v][kt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            const int key = 16 * kt + 4 * g4, val = val0 + 16 * v;
+            if (start && val < vw && key < a.kd)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    S[v][kt][r] = start[(int64_t)(v0 + val) * a.sv + (int64_t)(key + r) * a.sk];
+        }
 
-    u32x4 kr[KI], vr[VI];
-    Key qn[KIND == kEnds ? 1 : KK];
+    // Rows of the chunk ahead: a thread's pieces lie kRows rows apart, each read through a buffer of
+    // its own that begins at its rows, so that one offset in a register serves them all.
+    u32x4 kr[KI], vr[VI], qr[QI];
     float gn = 0.0f;
+    const int krow = tid / (DK / kVec), kcol = tid % (DK / kVec) * kVec;
+    const int vrow = tid / (BV / kVec), vcol = tid % (BV / kVec) * kVec;
+    const auto rows_at = [&](const T *base, int64_t pitch, int t, int rows, int width) {
+        return make_rsrc(base + t * pitch, (int)(((rows - 1) * pitch + width) * (int64_t)sizeof(T)));
+    };
+    const uint32_t koff = kcol < a.kd ? (uint32_t)((krow * (int)a.kp + kcol) * (int)sizeof(T)) : ~0u;
+    const uint32_t qoff = kcol < a.kd ? (uint32_t)((krow * (int)a.qp + kcol) * (int)sizeof(T)) : ~0u;
+    const uint32_t voff = vcol < vw ? (uint32_t)((vrow * (int)a.vp + vcol) * (int)sizeof(T)) : ~0u;
     const auto fetch = [&](int c) {
-        const int t0 = c * kChunk, rows = min(kChunk, n - t0);
-        const rsrc_t rk = make_rsrc(kb + (int64_t)t0 * a.kp, (int)(((rows - 1) * a.kp + a.kd) * sizeof(T)));
-        const rsrc_t rv = make_rsrc(vbp + (int64_t)t0 * a.vp, (int)(((rows - 1) * a.vp + vw) * sizeof(T)));
-        const rsrc_t rq = make_rsrc(qb + (int64_t)t0 * a.qp, (int)(((rows - 1) * a.qp + a.kd) * sizeof(T)));
+        const int t0 = c * CH, rows = min(CH, n - t0);
 #pragma unroll
-        for (int i = 0; i < KI; ++i) {
-            const int p = tid + i * kThreads, row = p / (DK / kVec), col = p % (DK / kVec) * kVec;
-            kr[i] = buf_load_b128(rk, col < a.kd ? (uint32_t)((row * (int)a.kp + col) * (int)sizeof(T)) : ~0u);
-        }
+        for (int i = 0; i < KI; ++i)
+            kr[i] = buf_load_b128(rows_at(kb, a.kp, t0 + i * KR, rows - i * KR, a.kd), koff);
 #pragma unroll
-        for (int i = 0; i < VI; ++i) {
-            const int p = tid + i * kThreads, row = p / (kBlock / kVec), col = p % (kBlock / kVec) * kVec;
-            vr[i] = buf_load_b128(rv, col < vw ? (uint32_t)((row * (int)a.vp + col) * (int)sizeof(T)) : ~0u);
-        }
-        if constexpr (KIND != kEnds) {
+        for (int i = 0; i < VI; ++i)
+            vr[i] = buf_load_b128(rows_at(vbp, a.vp, t0 + i * VR, rows - i * VR, vw), voff);
+        if constexpr (kOuts)
 #pragma unroll
-            for (int kk = 0; kk < KK; ++kk) {
-                const int col = Tile<T>::kKeys * kk + Tile<T>::kStepKeys * g4;
-                qn[kk] = __builtin_bit_cast(Key, buf_load_b128(rq, col < a.kd
-                    ? (uint32_t)(((16 * wave + c16) * (int)a.qp + col) * (int)sizeof(T)) : ~0u));
-            }
-        }
+            for (int i = 0; i < KI; ++i)
+                qr[i] = buf_load_b128(rows_at(qb, a.qp, t0 + i * KR, rows - i * KR, a.kd), qoff);
         gn = 0.0f;
         if (a.decay != 0 && lane < rows)
             gn = a.decay == 1 ? ((const float *)a.g)[h]
                               : (float)((const T *)a.g)[(row0 + t0 + lane) * a.gp + h];
     };
-    // rows of the outputs (those behind the sequence and values behind the block dropped)
-    const auto store_out = [&](auto *base, int t0, int rows, int i, const f32x4 (&o)[4]) {
-        typedef std::remove_pointer_t<decltype(base)> O;
-        const int pitch = a.H * a.vd;
-        const rsrc_t ro = make_rsrc(base + ((row0 + t0) * a.H + h) * a.vd + v0,
-                                    ((rows - 1) * pitch + vw) * (int)sizeof(O));
+    // the decays' gradient: a chunk's parts of the waves, added up behind a barrier
+    const auto store_parts = [&](int c) {
+        const int t = c * CH + lane;
+        if (wave != 0 || lane >= CH || t >= n) return;
+        const int64_t at = (bh * a.nvb + vb) * a.L + t;
+        float part = 0.0f;
 #pragma unroll
-        for (int vt = 0; vt < 4; ++vt) {
-            const int v = 16 * vt + 4 * g4;
-            buf_store4(ro, v < vw ? (uint32_t)((i * pitch + v) * (int)sizeof(O)) : ~0u, o[vt], (O *)nullptr);
+        for (int w = 0; w < 4; ++w) part += sPart[w][lane];
+        if constexpr (KIND == kDq) {
+            a.part[at] = part;
+        } else {
+            float written = 0.0f, cross = 0.0f;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                written += sWritten[w][lane];
+                cross += sX[w];
+            }
+            a.part[at] = part - written;
+            a.written[at] = written;
+            if (lane == 0) a.cross[(bh * a.nvb + vb) * a.nchunks + c] = cross;
         }
     };
-    if (it0 < it1) fetch(REV ? nc - 1 - it0 : it0);
 
+    if constexpr (kOuts)      // scores across the diagonal stay zero
+        for (int i = tid; i < CH * PP; i += kThreads) sP[i] = (T)0.0f;
+    if (count > 0) fetch(REV ? c0 + count - 1 : c0);
+
+    // Of two workgroups on a compute unit (256 apart) one goes first: in step they would both be in
+    // products, or both in what lies between (out: 77 us against 81 with 16384 tokens of 16 heads
+    // of 128 x 128; the ends' walk gains from priority for the products instead, 48 against 51)
+    if (kOuts && (blockIdx.x >> 8 & 1)) __builtin_amdgcn_s_setprio(2);
+    int straight = KeyRows::straight(lane), paired = KeyRows::paired(lane), down = KeyRows::down(lane);
+    int vdown = ValRows::on(ValRows::down(lane), 16 * NV * wave);
     float passed = 1.0f;      // the decay over the segment
-    for (int it = it0; it < it1; ++it) {
-        const int c = REV ? nc - 1 - it : it;
-        const int t0 = c * kChunk, rows = min(kChunk, n - t0);
-        // the chunk into LDS: K, V, the state as the products read it, and the factors
+    int c = 0;
+    for (int it = 0; it < count; ++it) {
+        const int last_c = c;
+        c = REV ? c0 + count - 1 - it : c0 + it;
+        const int t0 = c * CH, rows = min(CH, n - t0);
+        // the chunk into LDS, and its factors
 #pragma unroll
         for (int i = 0; i < KI; ++i) {
-            const int p = tid + i * kThreads, row = p / (DK / kVec), col = p % (DK / kVec) * kVec;
-            *reinterpret_cast<u32x4 *>(sK + row * KP + col) = kr[i];
+            *reinterpret_cast<u32x4 *>(sK + KeyRows::at(krow + i * KR, kcol)) = kr[i];
+            if constexpr (kOuts) *reinterpret_cast<u32x4 *>(sQ + KeyRows::at(krow + i * KR, kcol)) = qr[i];
         }
 #pragma unroll
-        for (int i = 0; i < VI; ++i) {
-            const int p = tid + i * kThreads, row = p / (kBlock / kVec), col = p % (kBlock / kVec) * kVec;
-            *reinterpret_cast<u32x4 *>(sV + row * VP + col) = vr[i];
-        }
-        Key q[KIND == kEnds ? 1 : KK];
-        if constexpr (KIND != kEnds) {
-#pragma unroll
-            for (int kt = 0; kt < KT; ++kt) store4(sS + val * SP + 16 * kt + 4 * g4, S[kt]);
-#pragma unroll
-            for (int kk = 0; kk < KK; ++kk) q[kk] = qn[kk];
-        }
+        for (int i = 0; i < VI; ++i)
+            *reinterpret_cast<u32x4 *>(sV + ValRows::at(vrow + i * VR, vcol)) = vr[i];
         const float g2 = decay2(gn);
         const float ghi = __builtin_rintf(g2 * 256.0f) * (1.0f / 256.0f);
         const float hi = wave_inclusive_sum(ghi), lo = wave_inclusive_sum(g2 - ghi);
         const float hE = wave_read(hi, 63), lE = wave_read(lo, 63);
-        const float from_start = fast_exp2(hi + lo), to_end = fast_exp2((hE - hi) + (lE - lo));
         const float whole = fast_exp2(hE + lE);
         if (KIND == kEnds) passed *= whole;
-        if (wave == 0) {
+        if (wave == 0 && lane < CH) {
+            const float from_start = fast_exp2(hi + lo), to_end = fast_exp2((hE - hi) + (lE - lo));
             sHi[lane] = hi;
             sLo[lane] = lo;
             sIn[lane] = (REV ? to_end : from_start) * a.inter;
             sW[lane] = (REV ? from_start : to_end) * a.weight;
         }
         __syncthreads();
-        if (it + 1 < it1) fetch(REV ? c - 1 : c + 1);
+        if (kParts && it > 0) store_parts(last_c);
+        // hidden from the compiler, which would hold every address that follows from them in a
+        // register for all chunks
+        asm volatile("" : "+v"(straight), "+v"(paired), "+v"(down), "+v"(vdown));
 
-        if constexpr (KIND != kEnds) {
-            // what the state before the chunk gives
-            const int i = 16 * wave + c16;                     // this lane's target
-            f32x4 o[4] = {};
+        f32x4 o[NV][NI] = {};
+        Raw xr[kParts ? NV : 1][NI];
+        // the states before the chunk, out of the forward walk for the backward one, which asks for
+        // them early where registers allow
+        constexpr bool kAhead = KIND == kDk && sizeof(T) == 2;
+        Raw before[kAhead ? NV : 1][kAhead ? KT : 1];
+        const rsrc_t rs = make_rsrc(kParts ? (T *)a.states + (bh * a.nchunks + c) * size : nullptr,
+                                    (int)(size * sizeof(T)));
+        const auto state_off = [&](int v, int kt) {
+            const int key = 16 * kt + 4 * g4, val = val0 + 16 * v;
+            return val < vw && key < a.kd ? (uint32_t)(((v0 + val) * a.kd + key) * (int)sizeof(T)) : ~0u;
+        };
+        if constexpr (kAhead)
 #pragma unroll
-            for (int kk = 0; kk < KK; ++kk)
+            for (int v = 0; v < NV; ++v)
 #pragma unroll
-                for (int vt = 0; vt < 4; ++vt) {
-                    const Key s = *reinterpret_cast<const Key *>(
-                        sS + (16 * vt + c16) * SP + Tile<T>::kKeys * kk + Tile<T>::kStepKeys * g4);
-                    o[vt] = mma16(s, q[kk], o[vt]);
+                for (int kt = 0; kt < KT; ++kt) before[v][kt] = buf_load4(rs, state_off(v, kt), (T *)nullptr);
+        if constexpr (kOuts) {
+            if constexpr (kParts) {
+                // rows whose products with the outputs the decays' gradient takes
+#pragma unroll
+                for (int v = 0; v < NV; ++v) {
+                    const int val = val4 + 16 * v;
+                    const uint32_t off = val < vw ? (uint32_t)((c16 * (int)a.xp + val) * (int)sizeof(T)) : ~0u;
+#pragma unroll
+                    for (int i = 0; i < NI; ++i)
+                        xr[v][i] = buf_load4(rows_at(xb, a.xp, t0 + 16 * i, rows - 16 * i, vw), off, (T *)nullptr);
                 }
-            const float in = sIn[i];
-#pragma unroll
-            for (int vt = 0; vt < 4; ++vt) o[vt] *= in;
-
-            // partner rows of the gradient of the decays
-            float part = 0.0f;
-            Key xf[KIND == kDq ? BK : 1];
-            if constexpr (KIND == kDq || KIND == kDk) {
-                const rsrc_t rx = make_rsrc(xb + (int64_t)t0 * a.xp, (int)(((rows - 1) * a.xp + vw) * sizeof(T)));
-                if (i < rows) {
-                    const T *p = xb + (int64_t)(t0 + i) * a.xp;
-#pragma unroll
-                    for (int vt = 0; vt < 4; ++vt)
-                        if (16 * vt + 4 * g4 < vw) {
-                            const f32x4 x = load4(p + 16 * vt + 4 * g4);
-#pragma unroll
-                            for (int r = 0; r < 4; ++r) part += o[vt][r] * x[r];
-                        }
-                }
-                if constexpr (KIND == kDq)
-#pragma unroll
-                    for (int kk = 0; kk < BK; ++kk) {
-                        const int col = Tile<T>::kKeys * kk + Tile<T>::kStepKeys * g4;
-                        xf[kk] = __builtin_bit_cast(Key, buf_load_b128(rx, col < vw
-                            ? (uint32_t)((i * (int)a.xp + col) * (int)sizeof(T)) : ~0u));
-                    }
             }
-
-            // scores, two tiles of 16 sources at a time, and what the chunk's own tokens give
-            const float hi_i = sHi[i], lo_i = sLo[i];
+            // Scores: tile j of them is that of targets i and sources u, u <= i (back in time the
+            // other way round).  The tile's place is hidden from the compiler, which would hold
+            // every address that follows from it in a register for all chunks.
+            int first = wave;
+            asm volatile("" : "+s"(first));
 #pragma unroll
-            for (int pr = 0; pr < 2; ++pr) {
-                if (REV ? 2 * pr + 1 < wave : 2 * pr > wave) {
-                    if constexpr (KIND == kDq)
-                        if (c16 == 15)
+            for (int j0 = 0; j0 < kTiles; j0 += 4) {
+                const int j = j0 + first;
+                if (j >= kTiles) break;
+                const int row = j < 1 ? 0 : j < 3 ? 1 : j < 6 ? 2 : 3, col = j - row * (row + 1) / 2;
+                const int i = REV ? NI - 1 - row : row, u = REV ? NI - 1 - col : col;
+                f32x4 p = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                            for (int r = 0; r < 8; ++r) sC[wave][32 * pr + 16 * (r >> 2) + 4 * g4 + (r & 3)] = 0.0f;
-                    continue;
-                }
-                f32x4 p[2];
+                for (int kk = 0; kk < KK; ++kk)
+                    p = mma16(load_straight<DK>(sK, straight, u, kk), load_straight<DK>(sQ, straight, i, kk), p);
+                const float hi_t = sHi[16 * i + c16], lo_t = sLo[16 * i + c16];
+                const f32x4 hs = load4(sHi + 16 * u + 4 * g4), ls = load4(sLo + 16 * u + 4 * g4);
+                float e[4];
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const int s0 = 32 * pr + 16 * u;
-                    p[u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                    for (int kk = 0; kk < KK; ++kk) {
-                        const Key k = *reinterpret_cast<const Key *>(
-                            sK + (s0 + c16) * KP + Tile<T>::kKeys * kk + Tile<T>::kStepKeys * g4);
-                        p[u] = mma16(k, q[kk], p[u]);
-                    }
-                    const f32x4 hs = load4(sHi + s0 + 4 * g4), ls = load4(sLo + s0 + 4 * g4);
+                for (int r = 0; r < 4; ++r)
+                    e[r] = REV ? (hs[r] - hi_t) + (ls[r] - lo_t) : (hi_t - hs[r]) + (lo_t - ls[r]);
+                if (i == u)
+                    // on the diagonal; before the exponential, which is formed for every pair: nothing
+                    // not finite from a pair that does not count
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        // selections before the exponential, which is formed for every pair: no
-                        // branches, and nothing not finite from a pair that does not count
-                        const int t = s0 + 4 * g4 + r;
-                        const bool keep = REV ? t >= i : t <= i;
-                        float e = REV ? (hs[r] - hi_i) + (ls[r] - lo_i) : (hi_i - hs[r]) + (lo_i - ls[r]);
-                        e = keep ? e : 0.0f;
-                        const float x = keep ? p[u][r] : 0.0f;
-                        p[u][r] = x * a.intra * fast_exp2(e);
+                        const int d = c16 - (4 * g4 + r);
+                        const bool keep = REV ? d <= 0 : d >= 0;
+                        e[r] = keep ? e[r] : 0.0f;
+                        p[r] = keep ? p[r] : 0.0f;
                     }
-                    if constexpr (KIND == kDq) {
-                        // scores of the other pair: their products' sums by target and by source
-                        f32x4 m = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                        for (int kk = 0; kk < BK; ++kk) {
-                            const Key v = *reinterpret_cast<const Key *>(
-                                sV + (s0 + c16) * VP + Tile<T>::kKeys * kk + Tile<T>::kStepKeys * g4);
-                            m = mma16(v, xf[kk], m);
-                        }
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            const float prod = p[u][r] != 0.0f ? m[r] * p[u][r] : 0.0f;
-                            part += prod;
-                            const float col = columns_sum(prod);
-                            if (c16 == 15) sC[wave][s0 + 4 * g4 + r] = col;
-                        }
-                    }
-                }
-                const Src ps = pack_src<T>(p[0], p[1]);
-#pragma unroll
-                for (int vt = 0; vt < 4; ++vt)
-                    o[vt] = mma16(load_src(sV, VP, 32 * pr, 16 * vt, lane), ps, o[vt]);
+                for (int r = 0; r < 4; ++r) p[r] *= a.intra * fast_exp2(e[r]);
+                store4(sP + (16 * i + c16) * PP + paired_place<T>(u, g4), p);
             }
-            if constexpr (KIND == kDq || KIND == kDk) {
-                part = rows_sum(part);
-                if (KIND == kDq && g4 == 0) sZ[i] = part;
-                if (KIND == kDk && g4 == 0 && i < rows) a.part[(bh * a.nvb + vb) * a.L + t0 + i] = part;
-            }
-            if (a.o32) store_out((float *)a.o, t0, rows, i, o);
-            else store_out((T *)a.o, t0, rows, i, o);
 
-            if constexpr (KIND == kDq || KIND == kDk) {
-                // states before the chunk out of the forward walk; their products with the gradients
-                // of the states behind it in the backward one
-                float x = 0.0f;
-                T *sc = (T *)a.states + ((bh * a.nchunks + c) * a.vd + v0 + val) * a.kd;
+            // what the state before the chunk gives
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int kk = 0; kk < KK; ++kk) {
+                Frag q[NI];
+#pragma unroll
+                for (int i = 0; i < NI; ++i) q[i] = load_paired<DK>(sQ, paired, i, kk);
+#pragma unroll
+                for (int v = 0; v < NV; ++v) {
+                    const Frag f = of_accumulators<T>(S[v], kk);
+#pragma unroll
+                    for (int i = 0; i < NI; ++i) o[v][i] = mma16(f, q[i], o[v][i]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                const float in = sIn[16 * i + c16];
+#pragma unroll
+                for (int v = 0; v < NV; ++v) o[v][i] *= in;
+                if constexpr (KIND == kDk) {
+                    float dot = 0.0f;
+#pragma unroll
+                    for (int v = 0; v < NV; ++v) dot += dot4(o[v][i], as_floats(xr[v][i]));
+                    dot = rows_sum(dot);
+                    if (g4 == 0) sWritten[wave][16 * i + c16] = dot;
+                }
+            }
+        }
+
+        if constexpr (kParts) {
+            // the states before the chunk out of the forward walk; their products with the
+            // gradients of the states behind it in the backward one
+            float x = 0.0f;
+#pragma unroll
+            for (int v = 0; v < NV; ++v)
 #pragma unroll
                 for (int kt = 0; kt < KT; ++kt) {
-                    const int key = 16 * kt + 4 * g4;
-                    if (has_val && key < a.kd) {
-                        if (KIND == kDq) {
-                            store4(sc + key, S[kt]);
-                        } else {
-                            const f32x4 s = load4(sc + key);
-#pragma unroll
-                            for (int r = 0; r < 4; ++r) x += s[r] * S[kt][r];
-                        }
-                    }
+                    if constexpr (KIND == kDq) buf_store4(rs, state_off(v, kt), S[v][kt], (T *)nullptr);
+                    else if constexpr (kAhead) x += dot4(as_floats(before[v][kt]), S[v][kt]);
+                    else x += dot4(as_floats(buf_load4(rs, state_off(v, kt), (T *)nullptr)), S[v][kt]);
                 }
-                if constexpr (KIND == kDk) {
-                    x = rows_sum(columns_sum(x)) * whole;
-                    if (lane == 15) sX[wave] = x;
-                }
+            if constexpr (KIND == kDk) {
+                x = rows_sum(columns_sum(x)) * whole;
+                if (lane == 15) sX[wave] = x;
             }
         }
+
+        // the chunk ahead is asked for here, so that its rows hold no registers while the products
+        // above need them
+        __builtin_amdgcn_sched_barrier(0);
+        if (it + 1 < count) fetch(REV ? c - 1 : c + 1);
 
         // the state behind the chunk
+        Frag vf[MM][NV];
 #pragma unroll
-        for (int kt = 0; kt < KT; ++kt) S[kt] *= whole;
+        for (int m = 0; m < MM; ++m)
 #pragma unroll
-        for (int pr = 0; pr < 2; ++pr) {
-            const Src v = load_src(sV, VP, 32 * pr, 16 * wave, lane);
-            const f32x4 w0 = load4(sW + 32 * pr + 4 * g4), w1 = load4(sW + 32 * pr + 16 + 4 * g4);
-            f32x8 w;
+            for (int v = 0; v < NV; ++v) vf[m][v] = load_down<BV>(sV, vdown, m, v);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) { w[e] = w0[e]; w[4 + e] = w1[e]; }
-            if constexpr (sizeof(T) == 4) {
-                const Src wv = v * w;
+        for (int v = 0; v < NV; ++v)
 #pragma unroll
-                for (int kt = 0; kt < KT; ++kt)
-                    S[kt] = mma16(load_src(sK, KP, 32 * pr, 16 * kt, lane), wv, S[kt]);
-            } else {
-                bf16x8 wv[3];
-                split3(v, w, wv);
-                // four tiles side by side: a product's three parts wait for each other
+            for (int kt = 0; kt < KT; ++kt) S[v][kt] *= whole;
+        if (!kOuts) __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-                for (int kt = 0; kt < KT; kt += 4) {
-                    Src k[4];
+        for (int m = 0; m < MM; ++m) {
+            Frag w[NV][PARTS];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) k[i] = load_src(sK, KP, 32 * pr, 16 * (kt + i), lane);
+            for (int v = 0; v < NV; ++v) weigh(vf[m][v], sW, m, g4, w[v]);
+            asm volatile("" : "+v"(down));
+            __builtin_amdgcn_sched_barrier(0);
+            // tiles of keys side by side: a product's parts wait for each other
 #pragma unroll
-                    for (int e = 0; e < 3; ++e)
+            for (int kt = 0; kt < KT; kt += kSide) {
+                Frag k[kSide];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) S[kt + i] = mma16(k[i], wv[e], S[kt + i]);
-                }
+                for (int i = 0; i < kSide; ++i) k[i] = load_down<DK>(sK, down, m, kt + i);
+#pragma unroll
+                for (int e = 0; e < PARTS; ++e)
+#pragma unroll
+                    for (int i = 0; i < kSide; ++i)
+#pragma unroll
+                        for (int v = 0; v < NV; ++v) S[v][kt + i] = mma16(k[i], w[v][e], S[v][kt + i]);
             }
         }
+        if (!kOuts) __builtin_amdgcn_s_setprio(0);
         __syncthreads();
-        if (KIND == kDq && wave == 0 && lane < rows)
-            a.part[(bh * a.nvb + vb) * a.L + t0 + lane] =
-                sZ[lane] - (((sC[0][lane] + sC[1][lane]) + sC[2][lane]) + sC[3][lane]);
-        if (KIND == kDk && tid == 0)
-            a.cross[(bh * a.nvb + vb) * a.nchunks + c] = ((sX[0] + sX[1]) + sX[2]) + sX[3];
+
+        if constexpr (kOuts) {
+            // what the chunk's own tokens give: steps of sources that reach these targets
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+#pragma unroll
+                for (int m = 0; m < MM; ++m) {
+                    if (REV ? Tile<T>::kStep * (m + 1) <= 16 * i : Tile<T>::kStep * m > 16 * i) continue;
+                    const Frag p = *reinterpret_cast<const Frag *>(
+                        sP + (16 * i + c16) * PP + Tile<T>::kStep * m + Tile<T>::kPart * g4);
+#pragma unroll
+                    for (int v = 0; v < NV; ++v) o[v][i] = mma16(vf[m][v], p, o[v][i]);
+                }
+            if constexpr (kParts) {
+#pragma unroll
+                for (int i = 0; i < NI; ++i) {
+                    float dot = 0.0f;
+#pragma unroll
+                    for (int v = 0; v < NV; ++v) dot += dot4(o[v][i], as_floats(xr[v][i]));
+                    dot = rows_sum(dot);
+                    if (g4 == 0) sPart[wave][16 * i + c16] = dot;
+                }
+            }
+            // rows behind the sequence and values behind the block are dropped
+            const int pitch = a.H * a.vd;
+            const auto store = [&](auto *base) {
+                typedef std::remove_pointer_t<decltype(base)> O;
+                base += ((row0 + t0) * a.H + h) * a.vd + v0;
+#pragma unroll
+                for (int v = 0; v < NV; ++v) {
+                    const int val = val4 + 16 * v;
+                    const uint32_t off = val < vw ? (uint32_t)((c16 * pitch + val) * (int)sizeof(O)) : ~0u;
+#pragma unroll
+                    for (int i = 0; i < NI; ++i)
+                        buf_store4(make_rsrc(base + (int64_t)(16 * i) * pitch,
+                                             ((rows - 16 * i - 1) * pitch + vw) * (int)sizeof(O)),
+                                   off, o[v][i], (O *)nullptr);
+                }
+            };
+            if (a.o32) store((float *)a.o);
+            else store((T *)a.o);
+        }
+    }
+    if (kParts && count > 0) {
+        __syncthreads();
+        store_parts(c);
     }
 
-    if constexpr (KIND == kEnds) {
+    if constexpr (KIND == kEnds)
         if (tid == 0 && vb == 0) a.decays[bh * a.nseg + s] = passed;
-        if (has_val) {
-            float *p = a.ends + (bh * a.nseg + s + 1) * size + (int64_t)(v0 + val) * a.sv;
+    float *p = KIND == kEnds ? a.ends + (bh * a.nseg + s) * size
+               : a.last      ? a.last + bh * size
+                             : nullptr;
+    if (p)
 #pragma unroll
-            for (int kt = 0; kt < KT; ++kt)
+        for (int v = 0; v < NV; ++v)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int key = 16 * kt + 4 * g4 + r;
-                    if (key < a.kd) p[key * a.sk] = S[kt][r];
-                }
-        }
-    } else if (a.last && has_val && s == a.nseg - 1) {
-        float *p = a.last + bh * size + (int64_t)(v0 + val) * a.kd;
-#pragma unroll
-        for (int kt = 0; kt < KT; ++kt)
-            if (16 * kt + 4 * g4 < a.kd)
-                store4(p + 16 * kt + 4 * g4, S[kt]);
-    }
+            for (int kt = 0; kt < KT; ++kt) {
+                const int key = 16 * kt + 4 * g4, val = val0 + 16 * v;
+                if (val < vw && key < a.kd) store4(p + (int64_t)(v0 + val) * a.kd + key, S[v][kt]);
+            }
 }
 
 // ---------------------------------------------------------------------------
-// Starts of the segments of every head out of their ends, in place: a thread for four elements of a
-// head's state, eight segments' ends on their way at a time.
+// Starts of the segments of every head out of their ends, in place, and the last state: a thread
+// for four elements of a head's state, eight segments' ends on their way at a time.
 // ---------------------------------------------------------------------------
 __global__ __launch_bounds__(kThreads) void chain_kernel(float *ends, const float *__restrict__ decays,
-                                                         const float *__restrict__ init, int64_t quads,
+                                                         const float *init, float *last, int64_t quads,
                                                          int size4, int nseg)
 {
     constexpr int kAhead = 8;
@@ -599,8 +729,8 @@ __global__ __launch_bounds__(kThreads) void chain_kernel(float *ends, const floa
         float d[kAhead];
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
-            const int s = min(s0 + i, nseg - 2);
-            end[i] = p[(int64_t)(s + 1) * size4];
+            const int s = min(s0 + i, nseg - 1);
+            end[i] = p[(int64_t)s * size4];
             d[i] = decays[bh * nseg + s];
         }
 #pragma unroll
@@ -610,13 +740,18 @@ __global__ __launch_bounds__(kThreads) void chain_kernel(float *ends, const floa
             S = S * d[i] + end[i];
         }
     }
+    if (last) reinterpret_cast<f32x4 *>(last)[id] = S;
 }
 
 // ---------------------------------------------------------------------------
-// Gradient of the log decays, a wave for a chunk of a head, a lane for a token.  g_t scales all
-// that passes token t: read behind it or in it (u: reads of the chunk's start state, and pairs
-// within the chunk by their targets less by their sources, `read`), written before it and read
-// behind the chunk (`written`), and what passes the whole chunk (`cross`).
+// Gradient of the log decays, a wave for a chunk of a head, a lane for a token.  g_t scales every
+// product of a read in or behind token t with a write before it.  In t's chunk:
+//   read     all that is read by its tokens from t on, q . dq
+//   own      less what these tokens write themselves and the chunk reads, the part of k . dk from
+//            within the chunk (its pairs are the same rounded scores as in q . dq: what is on one
+//            side of t cancels but for fp32's sums, however small the rest)
+//   written  what its tokens before t write and is read behind the chunk, the other part of k . dk
+//   cross    and what passes the whole chunk, <S, dS>
 // ---------------------------------------------------------------------------
 template <typename T>
 __global__ __launch_bounds__(kThreads) void decay_gradient_kernel(DecayGradient a)
@@ -630,12 +765,12 @@ __global__ __launch_bounds__(kThreads) void decay_gradient_kernel(DecayGradient 
         const int h = (int)(bh % a.H);
         int n = a.L;
         if (a.lengths) n = min(max(a.lengths[b], 0), a.L);
-        const int t = c * kChunk + lane;
-        if (c * kChunk >= n) continue;
+        const int t = lane < a.chunk ? c * a.chunk + lane : n;
+        if (c * a.chunk >= n) continue;
         float read = 0.0f, written = 0.0f, cross = 0.0f;
         for (int i = 0; i < a.nvb; ++i) {
             if (t < n) {
-                read += a.read[(bh * a.nvb + i) * a.L + t];
+                read += a.read[(bh * a.nvb + i) * a.L + t] - a.own[(bh * a.nvb + i) * a.L + t];
                 written += a.written[(bh * a.nvb + i) * a.L + t];
             }
             cross += a.cross[(bh * a.nvb + i) * a.nchunks + c];
@@ -682,51 +817,80 @@ unsigned groups_for(int64_t work, int each)
     return (unsigned)(n < (1 << 20) ? n : (1 << 20));
 }
 
-template <typename T, int DK, bool REV, Kind KIND>
-hipError_t walk_go(Walk a, int64_t bh, hipStream_t st)
+template <typename T, int NV, bool REV, Kind KIND, int PARTS>
+hipError_t walk_by_key(const Walk &a, hipStream_t st)
 {
-    a.groups = bh * (KIND == kEnds ? a.nseg - 1 : a.nseg);
-    const int64_t blocks = (a.groups + 7) / 8 * 8 * a.nvb;
-    hipLaunchKernelGGL((walk_kernel<T, DK, REV, KIND>), dim3((unsigned)blocks), dim3(kThreads), 0, st, a);
+    const dim3 blocks((unsigned)((a.groups + 7) / 8 * 8 * a.nvb)), threads(kThreads);
+    if (a.kd <= 64)
+        hipLaunchKernelGGL((walk_kernel<T, 64, NV, REV, KIND, PARTS>), blocks, threads, 0, st, a);
+    else if (a.kd <= 128)
+        hipLaunchKernelGGL((walk_kernel<T, 128, NV, REV, KIND, PARTS>), blocks, threads, 0, st, a);
+    else
+        hipLaunchKernelGGL((walk_kernel<T, 256, NV, REV, KIND, PARTS>), blocks, threads, 0, st, a);
     return hipGetLastError();
 }
 
-template <typename T, bool REV, Kind KIND>
-hipError_t walk_by_key(const Walk &a, int64_t bh, hipStream_t st)
+// Values of a walk: 64, or 128 (bf16, without a part in the decays' gradient) where there are more.
+int block_of(bool bf16, Kind kind, int64_t values)
 {
-    if (a.kd <= 64) return walk_go<T, 64, REV, KIND>(a, bh, st);
-    if (a.kd <= 128) return walk_go<T, 128, REV, KIND>(a, bh, st);
-    return walk_go<T, 256, REV, KIND>(a, bh, st);
+    return bf16 && (kind == kEnds || kind == kOut) && values > 64 ? 128 : 64;
+}
+int blocks_of(bool bf16, Kind kind, int64_t values)
+{
+    const int block = block_of(bf16, kind, values);
+    return (int)((values + block - 1) / block);
 }
 
-// The ends of a walk's segments, and their starts.
-template <typename T, bool REV> hipError_t starts_go(const Walk &a, int64_t bh, hipStream_t st)
+template <typename T, bool REV, Kind KIND> hipError_t walk_launch(Walk a, int64_t bh, hipStream_t st)
 {
-    const hipError_t e = walk_by_key<T, REV, kEnds>(a, bh, st);
+    a.groups = bh * a.nseg;
+    a.nvb = blocks_of(sizeof(T) == 2, KIND, a.vd);
+    if constexpr (sizeof(T) == 4) {
+        return walk_by_key<T, 1, REV, KIND, 1>(a, st);
+    } else if constexpr (KIND == kDq || KIND == kDk) {
+        return walk_by_key<T, 1, REV, KIND, 2>(a, st);
+    } else {
+        const bool wide = block_of(true, KIND, a.vd) == 128;
+        if (KIND == kEnds || a.last)
+            return wide ? walk_by_key<T, 2, REV, KIND, 3>(a, st) : walk_by_key<T, 1, REV, KIND, 3>(a, st);
+        if constexpr (KIND == kOut)
+            return wide ? walk_by_key<T, 2, REV, KIND, 2>(a, st) : walk_by_key<T, 1, REV, KIND, 2>(a, st);
+        return hipErrorInvalidValue;
+    }
+}
+
+// The ends of a walk's segments, then their starts and the last state.
+template <typename T, bool REV> hipError_t starts_go(const Walk &a, float *last, int64_t bh, hipStream_t st)
+{
+    const hipError_t e = walk_launch<T, REV, kEnds>(a, bh, st);
     if (e != hipSuccess) return e;
     const int size4 = a.kd * a.vd / 4;
     const int64_t quads = bh * size4;
     hipLaunchKernelGGL(chain_kernel, dim3((unsigned)((quads + kThreads - 1) / kThreads)), dim3(kThreads), 0,
-                       st, a.ends, a.decays, a.init, quads, size4, a.nseg);
+                       st, a.ends, a.decays, a.init, last, quads, size4, a.nseg);
     return hipGetLastError();
 }
 
-int blocks_of(int64_t values) { return (int)((values + kBlock - 1) / kBlock); }
 
 // How the chunks of a walk are split into segments, whose ends a first walk leaves.
 struct Split {
     int seg, nseg;
 };
-Split split_of(int64_t walks, int chunks)
+Split split_of(int64_t walks, int64_t tokens)
 {
     constexpr int kWant = 512, kLeast = 4;
-    const int64_t n = (kWant + walks - 1) / walks;
-    int seg = (int)((chunks + n - 1) / n);
+    const int64_t chunks = (tokens + 63) / 64, n = (kWant + walks - 1) / walks;
+    int64_t seg = (chunks + n - 1) / n;
     if (seg < kLeast) seg = kLeast;
-    return {seg, (chunks + seg - 1) / seg};
+    return {(int)seg * 64, (int)((chunks + seg - 1) / seg)};
 }
 
-int chunks_of(const LinattnShape &s) { return (int)((s.L + kChunk - 1) / kChunk); }
+// Chunks of the walks that leave parts of the decays' gradient (their keys are the values).
+int part_chunks(const LinattnShape &s)
+{
+    const int n = chunk_tokens(s.bf16, s.dv);
+    return (int)((s.L + n - 1) / n);
+}
 
 // Workspace of one split: ends and decays (byte offsets).
 int64_t ends_bytes(const LinattnShape &s, int nseg)
@@ -739,19 +903,18 @@ int64_t decays_bytes(const LinattnShape &s, int nseg)
 }
 Split forward_split(const LinattnShape &s)
 {
-    return split_of(s.b * s.H * blocks_of(s.dv), chunks_of(s));
+    return split_of(s.b * s.H * blocks_of(s.bf16, kOut, s.dv), s.L);
 }
 
 Split grad_split(const LinattnShape &s)
 {
-    const int64_t least = blocks_of(s.dk) < blocks_of(s.dv) ? blocks_of(s.dk) : blocks_of(s.dv);
-    return split_of(s.b * s.H * least, chunks_of(s));
+    return split_of(s.b * s.H * std::min(blocks_of(s.bf16, kOut, s.dk), blocks_of(s.bf16, kOut, s.dv)), s.L);
 }
 
 // Workspace of the gradients (byte offsets, on 256 bytes): with a decays' gradient the states
 // before each chunk and the parts that its kernel adds up; with shared heads every head's dq and dk.
 struct GradLayout {
-    int64_t states, read, written, cross, dq, dk, ends, decays, back_ends, back_decays, bytes;
+    int64_t states, read, own, written, cross, dq, dk, ends, decays, back_ends, back_decays, bytes;
     Split split;
 };
 GradLayout grad_layout(const LinattnShape &s, bool gates)
@@ -763,9 +926,10 @@ GradLayout grad_layout(const LinattnShape &s, bool gates)
         if (wanted) at += (bytes + 255) / 256 * 256;
         return off;
     };
-    const int64_t bh = s.b * s.H, nvb = blocks_of(s.dk), nc = chunks_of(s);
+    const int64_t bh = s.b * s.H, nvb = blocks_of(s.bf16, kDq, s.dk), nc = part_chunks(s);
     y.states = take(gates, bh * nc * s.dk * s.dv * (s.bf16 ? 2 : 4));
     y.read = take(gates, bh * nvb * s.L * 4);
+    y.own = take(gates, bh * nvb * s.L * 4);
     y.written = take(gates, bh * nvb * s.L * 4);
     y.cross = take(gates, bh * nvb * nc * 4);
     const int64_t heads = s.b * s.L * s.H * s.dk * 4;
@@ -793,16 +957,16 @@ template <typename T> hipError_t forward_go(const LinattnShape &s, const Linattn
     w.weight = 1.0f;
     w.inter = w.intra = s.scale;
     w.L = (int)s.L; w.H = (int)s.H; w.kd = (int)s.dk; w.vd = (int)s.dv;
-    w.nvb = blocks_of(s.dv);
     const Split y = forward_split(s);
     w.seg = y.seg; w.nseg = y.nseg;
     w.ends = (float *)a.ws;
     w.decays = (float *)((char *)a.ws + ends_bytes(s, y.nseg));
     if (y.nseg > 1) {
-        const hipError_t e = starts_go<T, false>(w, s.b * s.H, st);
+        const hipError_t e = starts_go<T, false>(w, w.last, s.b * s.H, st);
         if (e != hipSuccess) return e;
+        w.last = nullptr;
     }
-    return walk_by_key<T, false, kOut>(w, s.b * s.H, st);
+    return walk_launch<T, false, kOut>(w, s.b * s.H, st);
 }
 
 // Gradients: three walks (q's forward in time, then k's and v's back), the decays' from the parts
@@ -821,7 +985,7 @@ hipError_t backward_go(const LinattnShape &s, const LinattnGradArgs &a, hipStrea
     Walk w = {};
     w.g = a.g; w.gp = s.gp; w.decay = s.decay; w.lengths = a.lengths;
     w.L = (int)s.L; w.H = (int)s.H;
-    w.nchunks = chunks_of(s);
+    w.nchunks = part_chunks(s);
     w.states = at(y.states);
     w.cross = (float *)at(y.cross);
 
@@ -840,10 +1004,10 @@ hipError_t backward_go(const LinattnShape &s, const LinattnGradArgs &a, hipStrea
         for (Walk *x : {&f, &r}) {
             x->qdiv = 1;
             x->sv = s.dk; x->sk = 1;
-            x->kd = (int)s.dk; x->vd = (int)s.dv; x->nvb = blocks_of(s.dv);
+            x->kd = (int)s.dk; x->vd = (int)s.dv;
         }
-        e = starts_go<T, false>(f, bh, st);
-        if (e == hipSuccess) e = starts_go<T, true>(r, bh, st);
+        e = starts_go<T, false>(f, nullptr, bh, st);
+        if (e == hipSuccess) e = starts_go<T, true>(r, a.dh0, bh, st);
         if (e != hipSuccess) return e;
     }
 
@@ -854,10 +1018,10 @@ hipError_t backward_go(const LinattnShape &s, const LinattnGradArgs &a, hipStrea
     q.o = share > 1 ? at(y.dq) : a.dq; q.o32 = share > 1;
     q.init = a.h0; q.sv = 1; q.sk = s.dk;
     q.inter = q.intra = s.scale; q.weight = 1.0f;
-    q.kd = (int)s.dv; q.vd = (int)s.dk; q.nvb = blocks_of(s.dk);
+    q.kd = (int)s.dv; q.vd = (int)s.dk;
     q.x = a.q; q.xp = s.qp; q.xdiv = share;
     q.part = (float *)at(y.read);
-    e = gates ? walk_by_key<T, false, kDq>(q, bh, st) : walk_by_key<T, false, kOut>(q, bh, st);
+    e = gates ? walk_launch<T, false, kDq>(q, bh, st) : walk_launch<T, false, kOut>(q, bh, st);
     if (e != hipSuccess) return e;
 
     Walk k = back;       // dk = dS^T v, scale in dS
@@ -867,10 +1031,10 @@ hipError_t backward_go(const LinattnShape &s, const LinattnGradArgs &a, hipStrea
     k.o = share > 1 ? at(y.dk) : a.dk; k.o32 = share > 1;
     k.init = a.dhT; k.sv = 1; k.sk = s.dk;
     k.inter = 1.0f; k.intra = k.weight = s.scale;
-    k.kd = (int)s.dv; k.vd = (int)s.dk; k.nvb = blocks_of(s.dk);
+    k.kd = (int)s.dv; k.vd = (int)s.dk;
     k.x = a.k; k.xp = s.kp; k.xdiv = share;
-    k.part = (float *)at(y.written);
-    e = gates ? walk_by_key<T, true, kDk>(k, bh, st) : walk_by_key<T, true, kOut>(k, bh, st);
+    k.part = (float *)at(y.own); k.written = (float *)at(y.written);
+    e = gates ? walk_launch<T, true, kDk>(k, bh, st) : walk_launch<T, true, kOut>(k, bh, st);
     if (e != hipSuccess) return e;
 
     Walk v = back;       // dv = dS k
@@ -879,18 +1043,19 @@ hipError_t backward_go(const LinattnShape &s, const LinattnGradArgs &a, hipStrea
     v.v = a.dout; v.vp = s.dop; v.vdiv = 1;
     v.o = a.dv;
     v.init = a.dhT; v.sv = s.dk; v.sk = 1;
-    v.last = a.dh0;
+    v.last = v.nseg > 1 ? nullptr : a.dh0;
     v.inter = 1.0f; v.intra = v.weight = s.scale;
-    v.kd = (int)s.dk; v.vd = (int)s.dv; v.nvb = blocks_of(s.dv);
-    e = walk_by_key<T, true, kOut>(v, bh, st);
+    v.kd = (int)s.dk; v.vd = (int)s.dv;
+    e = walk_launch<T, true, kOut>(v, bh, st);
     if (e != hipSuccess) return e;
 
     if (gates) {
         DecayGradient d = {};
         d.g = a.g; d.gp = s.gp; d.lengths = a.lengths;
-        d.read = q.part; d.written = k.part; d.cross = w.cross;
+        d.read = q.part; d.own = k.part; d.written = k.written; d.cross = w.cross;
         d.dg = a.dg;
-        d.bh = bh; d.L = (int)s.L; d.H = (int)s.H; d.nvb = q.nvb; d.nchunks = w.nchunks;
+        d.bh = bh; d.L = (int)s.L; d.H = (int)s.H; d.nvb = blocks_of(s.bf16, kDq, s.dk);
+        d.nchunks = w.nchunks; d.chunk = chunk_tokens(s.bf16, s.dv);
         hipLaunchKernelGGL((decay_gradient_kernel<T>), dim3(groups_for(bh * w.nchunks, 4)), dim3(kThreads),
                            0, st, d);
         e = hipGetLastError();

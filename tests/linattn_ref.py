@@ -203,6 +203,9 @@ def backward(do, q, k, v, g, h0, dhT, scale, lengths=None):
     n = q.shape[3] + v.shape[3] + 2 * CHUNK + 4 * p.chunks + 32
     bound = U * (n * (A + 2 * inside) + 2 * E) + NOTHING
     if bf16:
+        # the scores of pairs within a chunk, rounded once, the same in q . dq and in k . dk: half a
+        # step of each product that passes t, and nothing of one that does not
+        bound = bound + HALF * passing(pairs.abs() * p.same)
         # reads and writes of rounded states, and rounded states against their gradients
         for c in range(p.chunks):
             s = slice(c * CHUNK, min((c + 1) * CHUNK, L))
