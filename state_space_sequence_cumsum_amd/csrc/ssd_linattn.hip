@@ -400,30 +400,35 @@ __global__ __launch_bounds__(kThreads, (waves_for<T, DK, NV>())) void walk_kerne
                     S[v][kt][r] = start[(int64_t)(v0 + val) * a.sv + (int64_t)(key + r) * a.sk];
         }
 
-    // Rows of the chunk ahead: a thread's pieces lie kRows rows apart, each read through a buffer of
-    // its own that begins at its rows, so that one offset in a register serves them all.
+    // Rows of the chunk ahead: a thread's pieces lie KR (VR) rows apart.  Offsets are bytes from the
+    // chunk's first row, below 2^30; kNowhere and what is added to it lies past every buffer's end.
+    constexpr uint32_t kNowhere = 1u << 31;
     u32x4 kr[KI], vr[VI], qr[QI];
     float gn = 0.0f;
     const int krow = tid / (DK / kVec), kcol = tid % (DK / kVec) * kVec;
     const int vrow = tid / (BV / kVec), vcol = tid % (BV / kVec) * kVec;
     const auto rows_at = [&](const T *base, int64_t pitch, int t, int rows, int width) {
-        return make_rsrc(base + t * pitch, (int)(((rows - 1) * pitch + width) * (int64_t)sizeof(T)));
+        return make_rsrc(base + t * pitch, ((rows - 1) * (int)pitch + width) * (int)sizeof(T));
     };
-    const uint32_t koff = kcol < a.kd ? (uint32_t)((krow * (int)a.kp + kcol) * (int)sizeof(T)) : ~0u;
-    const uint32_t qoff = kcol < a.kd ? (uint32_t)((krow * (int)a.qp + kcol) * (int)sizeof(T)) : ~0u;
-    const uint32_t voff = vcol < vw ? (uint32_t)((vrow * (int)a.vp + vcol) * (int)sizeof(T)) : ~0u;
+    const auto bytes = [](int row, int64_t pitch, int col) {
+        return (uint32_t)((row * (int)pitch + col) * (int)sizeof(T));
+    };
+    uint32_t koff = kcol < a.kd ? bytes(krow, a.kp, kcol) : kNowhere;
+    uint32_t qoff = kcol < a.kd ? bytes(krow, a.qp, kcol) : kNowhere;
+    uint32_t voff = vcol < vw ? bytes(vrow, a.vp, vcol) : kNowhere;
     const auto fetch = [&](int c) {
         const int t0 = c * CH, rows = min(CH, n - t0);
+        const rsrc_t rk = rows_at(kb, a.kp, t0, rows, a.kd), rv = rows_at(vbp, a.vp, t0, rows, vw);
+        asm volatile("" : "+v"(koff), "+v"(qoff), "+v"(voff));      // (as the places in LDS below)
 #pragma unroll
-        for (int i = 0; i < KI; ++i)
-            kr[i] = buf_load_b128(rows_at(kb, a.kp, t0 + i * KR, rows - i * KR, a.kd), koff);
+        for (int i = 0; i < KI; ++i) kr[i] = buf_load_b128(rk, koff + bytes(i * KR, a.kp, 0));
 #pragma unroll
-        for (int i = 0; i < VI; ++i)
-            vr[i] = buf_load_b128(rows_at(vbp, a.vp, t0 + i * VR, rows - i * VR, vw), voff);
-        if constexpr (kOuts)
+        for (int i = 0; i < VI; ++i) vr[i] = buf_load_b128(rv, voff + bytes(i * VR, a.vp, 0));
+        if constexpr (kOuts) {
+            const rsrc_t rq = rows_at(qb, a.qp, t0, rows, a.kd);
 #pragma unroll
-            for (int i = 0; i < KI; ++i)
-                qr[i] = buf_load_b128(rows_at(qb, a.qp, t0 + i * KR, rows - i * KR, a.kd), qoff);
+            for (int i = 0; i < KI; ++i) qr[i] = buf_load_b128(rq, qoff + bytes(i * KR, a.qp, 0));
+        }
         gn = 0.0f;
         if (a.decay != 0 && lane < rows)
             gn = a.decay == 1 ? ((const float *)a.g)[h]
@@ -516,13 +521,13 @@ __global__ __launch_bounds__(kThreads, (waves_for<T, DK, NV>())) void walk_kerne
         if constexpr (kOuts) {
             if constexpr (kParts) {
                 // rows whose products with the outputs the decays' gradient takes
+                const rsrc_t rx = rows_at(xb, a.xp, t0, rows, vw);
 #pragma unroll
                 for (int v = 0; v < NV; ++v) {
-                    const int val = val4 + 16 * v;
-                    const uint32_t off = val < vw ? (uint32_t)((c16 * (int)a.xp + val) * (int)sizeof(T)) : ~0u;
+                    const uint32_t off = val4 + 16 * v < vw ? bytes(c16, a.xp, val4 + 16 * v) : kNowhere;
 #pragma unroll
                     for (int i = 0; i < NI; ++i)
-                        xr[v][i] = buf_load4(rows_at(xb, a.xp, t0 + 16 * i, rows - 16 * i, vw), off, (T *)nullptr);
+                        xr[v][i] = buf_load4(rx, off + bytes(16 * i, a.xp, 0), (T *)nullptr);
                 }
             }
             // Scores: tile j of them is that of targets i and sources u, u <= i (back in time the
@@ -674,16 +679,40 @@ __global__ __launch_bounds__(kThreads, (waves_for<T, DK, NV>())) void walk_kerne
             const int pitch = a.H * a.vd;
             const auto store = [&](auto *base) {
                 typedef std::remove_pointer_t<decltype(base)> O;
-                base += ((row0 + t0) * a.H + h) * a.vd + v0;
+                const rsrc_t ro = make_rsrc(base + ((row0 + t0) * a.H + h) * a.vd + v0,
+                                            ((rows - 1) * pitch + vw) * (int)sizeof(O));
+                const auto place = [&](int row, int val) {
+                    return val < vw ? (uint32_t)((row * pitch + val) * (int)sizeof(O)) : kNowhere;
+                };
+                if constexpr (sizeof(O) == 2 && NV == 2) {
+                    // Two tiles of values side by side: lanes of odd rows of 16 give their first tile's
+                    // four to the row before them and take its second tile's, so that each holds
+                    // eight values of one tile, 16 bytes, and four lanes 64 bytes of a row.
+                    uint32_t off = place(c16, 16 * NV * wave + 16 * (g4 & 1) + 8 * (g4 >> 1));
 #pragma unroll
-                for (int v = 0; v < NV; ++v) {
-                    const int val = val4 + 16 * v;
-                    const uint32_t off = val < vw ? (uint32_t)((c16 * pitch + val) * (int)sizeof(O)) : ~0u;
+                    for (int i = 0; i < NI; ++i) {
+                        u32x4 w;
 #pragma unroll
-                    for (int i = 0; i < NI; ++i)
-                        buf_store4(make_rsrc(base + (int64_t)(16 * i) * pitch,
-                                             ((rows - 16 * i - 1) * pitch + vw) * (int)sizeof(O)),
-                                   off, o[v][i], (O *)nullptr);
+                        for (int j = 0; j < 2; ++j) {
+                            const auto x = __builtin_amdgcn_permlane16_swap(
+                                pack_bf16(o[0][i][2 * j], o[0][i][2 * j + 1]),
+                                pack_bf16(o[1][i][2 * j], o[1][i][2 * j + 1]), false, false);
+                            w[j] = x[0];
+                            w[2 + j] = x[1];
+                        }
+                        buf_store_b128(ro, off, w);
+                        off += (uint32_t)(16 * pitch * (int)sizeof(O));
+                    }
+                } else {
+#pragma unroll
+                    for (int v = 0; v < NV; ++v) {
+                        uint32_t off = place(c16, val4 + 16 * v);
+#pragma unroll
+                        for (int i = 0; i < NI; ++i) {
+                            buf_store4(ro, off, o[v][i], (O *)nullptr);
+                            off += (uint32_t)(16 * pitch * (int)sizeof(O));
+                        }
+                    }
                 }
             };
             if (a.o32) store((float *)a.o);
