@@ -270,7 +270,16 @@ __device__ __forceinline__ void buf_store4(rsrc_t r, uint32_t off, const f32x4 &
 {
     buf_store_b128(r, off, __builtin_bit_cast(u32x4, v));
 }
-// Four elements as they come, and as fp32.
+// One element as it comes, and as fp32; four.
+__device__ __forceinline__ uint32_t buf_load1(rsrc_t r, uint32_t off, bf16 *)
+{
+    return (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, (int)off, 0, 0);
+}
+__device__ __forceinline__ uint32_t buf_load1(rsrc_t r, uint32_t off, float *) { return buf_load_b32(r, off); }
+template <typename T> __device__ __forceinline__ float as_float(uint32_t v)
+{
+    return __uint_as_float(sizeof(T) == 2 ? v << 16 : v);
+}
 template <typename T> struct Raw4;
 template <> struct Raw4<bf16> { typedef u2 t; };
 template <> struct Raw4<float> { typedef u32x4 t; };
@@ -404,7 +413,8 @@ __global__ __launch_bounds__(kThreads, (waves_for<T, DK, NV>())) void walk_kerne
     // chunk's first row, below 2^30; kNowhere and what is added to it lies past every buffer's end.
     constexpr uint32_t kNowhere = 1u << 31;
     u32x4 kr[KI], vr[VI], qr[QI];
-    float gn = 0.0f;
+    uint32_t gn = 0;
+    const float ghead = a.decay == SSD_DECAY_HEAD ? ((const float *)a.g)[h] : 0.0f;
     const int krow = tid / (DK / kVec), kcol = tid % (DK / kVec) * kVec;
     const int vrow = tid / (BV / kVec), vcol = tid % (BV / kVec) * kVec;
     const auto rows_at = [&](const T *base, int64_t pitch, int t, int rows, int width) {
@@ -416,6 +426,7 @@ __global__ __launch_bounds__(kThreads, (waves_for<T, DK, NV>())) void walk_kerne
     uint32_t koff = kcol < a.kd ? bytes(krow, a.kp, kcol) : kNowhere;
     uint32_t qoff = kcol < a.kd ? bytes(krow, a.qp, kcol) : kNowhere;
     uint32_t voff = vcol < vw ? bytes(vrow, a.vp, vcol) : kNowhere;
+    const uint32_t goff = bytes(lane, a.gp, h);
     const auto fetch = [&](int c) {
         const int t0 = c * CH, rows = min(CH, n - t0);
         const rsrc_t rk = rows_at(kb, a.kp, t0, rows, a.kd), rv = rows_at(vbp, a.vp, t0, rows, vw);
@@ -429,10 +440,9 @@ __global__ __launch_bounds__(kThreads, (waves_for<T, DK, NV>())) void walk_kerne
 #pragma unroll
             for (int i = 0; i < KI; ++i) qr[i] = buf_load_b128(rq, qoff + bytes(i * KR, a.qp, 0));
         }
-        gn = 0.0f;
-        if (a.decay != 0 && lane < rows)
-            gn = a.decay == 1 ? ((const float *)a.g)[h]
-                              : (float)((const T *)a.g)[(row0 + t0 + lane) * a.gp + h];
+        // as it comes: a conversion here would wait for all of these loads
+        if (a.decay == SSD_DECAY_TOKEN)
+            gn = buf_load1(rows_at((const T *)a.g + row0 * a.gp, a.gp, t0, rows, a.H), goff, (T *)nullptr);
     };
     // the decays' gradient: a chunk's parts of the waves, added up behind a barrier
     const auto store_parts = [&](int c) {
@@ -482,7 +492,7 @@ __global__ __launch_bounds__(kThreads, (waves_for<T, DK, NV>())) void walk_kerne
 #pragma unroll
         for (int i = 0; i < VI; ++i)
             *reinterpret_cast<u32x4 *>(sV + ValRows::at(vrow + i * VR, vcol)) = vr[i];
-        const float g2 = decay2(gn);
+        const float g2 = decay2(a.decay == SSD_DECAY_TOKEN ? as_float<T>(gn) : lane < rows ? ghead : 0.0f);
         const float ghi = __builtin_rintf(g2 * 256.0f) * (1.0f / 256.0f);
         const float hi = wave_inclusive_sum(ghi), lo = wave_inclusive_sum(g2 - ghi);
         const float hE = wave_read(hi, 63), lE = wave_read(lo, 63);
