@@ -911,16 +911,26 @@ template <typename T, bool REV> hipError_t starts_go(const Walk &a, float *last,
 }
 
 
-// How the chunks of a walk are split into segments, whose ends a first walk leaves.
+// How the chunks of a walk are split into segments, whose ends a first walk leaves.  `keys`: of the
+// widest state.  As many segments as workgroups fit at once: of 24 heads of 2 x 2048 tokens of 128 x 64
+// 384 take 44 us and 528, some of which wait for others, 52; 16384 tokens of 16 heads of 128 x 128 take
+// 126 us in 512 and 165 in 1024, 4096 of 4 heads of 256 x 256 60 in 256 and 90 in 512.  While each
+// has a CU to itself a segment may be one chunk; else it is two or more, as the chain over the
+// segments is then the longer part (4 x 1024 tokens of 8 heads of 128 x 128: 37 us with two, 46 with one).
+// Segments are walked twice, and their ends and the chain are launches that take about the time of
+// two chunks (fp32: one), so there are none unless that is less than one walk over all: 256
+// tokens of 8 bf16 heads of 128 x 128 take 21 us in one walk and 24 in four segments, the gradients of 256
+// of 4 fp32 heads of 64 x 64 87 and 50.
 struct Split {
     int seg, nseg;
 };
-Split split_of(int64_t walks, int64_t tokens)
+Split split_of(bool is_bf16, int64_t keys, int64_t walks, int64_t tokens)
 {
-    constexpr int kWant = 512, kLeast = 4;
-    const int64_t chunks = (tokens + 63) / 64, n = (kWant + walks - 1) / walks;
+    const int64_t fit = (is_bf16 ? keys <= 128 : keys <= 64) ? 512 : 256;
+    const int64_t chunks = (tokens + 63) / 64, n = std::max<int64_t>(fit / walks, 1);
     int64_t seg = (chunks + n - 1) / n;
-    if (seg < kLeast) seg = kLeast;
+    if (seg == 1 && walks * chunks > 256) seg = 2;
+    if (2 * seg + (is_bf16 ? 2 : 1) >= chunks) seg = chunks;
     return {(int)seg * 64, (int)((chunks + seg - 1) / seg)};
 }
 
@@ -942,12 +952,13 @@ int64_t decays_bytes(const LinattnShape &s, int nseg)
 }
 Split forward_split(const LinattnShape &s)
 {
-    return split_of(s.b * s.H * blocks_of(s.bf16, kOut, s.dv), s.L);
+    return split_of(s.bf16, s.dk, s.b * s.H * blocks_of(s.bf16, kOut, s.dv), s.L);
 }
 
 Split grad_split(const LinattnShape &s)
 {
-    return split_of(s.b * s.H * std::min(blocks_of(s.bf16, kOut, s.dk), blocks_of(s.bf16, kOut, s.dv)), s.L);
+    return split_of(s.bf16, std::max(s.dk, s.dv),
+                    s.b * s.H * std::min(blocks_of(s.bf16, kOut, s.dk), blocks_of(s.bf16, kOut, s.dv)), s.L);
 }
 
 // Workspace of the gradients (byte offsets, on 256 bytes): with a decays' gradient the states
