@@ -5,7 +5,10 @@
 // in place on the fp32 state [value, key] of every (batch, head).  The step reads and writes the
 // state once and does five operations for each of its elements: bound by HBM, or by launch latency at
 // small batches.  A team of lanes holds a row, 16 bytes a lane, with its q and k in registers; a
-// wave's teams take kRows rows each.
+// wave's teams take kRows rows each (of 128 x 16 heads of 128 x 128 two take 50 us, four 49, eight
+// 49; of 16 x 16 heads 7.7, 7.8 and 10.3).  A state too large to stay in the caches until the next step goes
+// past them: 128 x 16 heads then take 49 us (5.5 TB/s) instead of 60, 16 x 16 7.8 instead of 9.8; 8 x 16,
+// which stay in L2 when the same state steps again, 5.8 instead of 5.0.
 #include <hip/hip_runtime.h>
 
 #include "ssd_device.h"
@@ -14,8 +17,9 @@
 namespace ssd {
 namespace {
 
-constexpr int kRows = 4;        // rows of a team
 constexpr int kStepThreads = 256;
+constexpr int kRows = 4;        // rows of a team
+constexpr int64_t kCached = 10 << 20;
 
 __device__ __forceinline__ f32x4 load4(const float *p) { return *reinterpret_cast<const f32x4 *>(p); }
 __device__ __forceinline__ f32x4 load4(const bf16 *p)
@@ -32,7 +36,8 @@ struct StepDims {
     float scale;
 };
 
-template <typename T, int TEAM>
+// Streams: the state goes past the caches.
+template <typename T, int TEAM, bool STREAM>
 __global__ __launch_bounds__(kStepThreads) void linattn_step_kernel(
     const T *__restrict__ q, const T *__restrict__ k, const T *v, const void *__restrict__ g,
     float *__restrict__ h, T *o, StepDims m)
@@ -52,7 +57,10 @@ __global__ __launch_bounds__(kStepThreads) void linattn_step_kernel(
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
         const bool row = row0 + r * kTeams < m.dv;
-        s[r] = in && row ? load4(hp + (int64_t)r * kTeams * m.dk) : zero;
+        const float *at = hp + (int64_t)r * kTeams * m.dk;
+        s[r] = !(in && row) ? zero
+               : STREAM     ? __builtin_nontemporal_load(reinterpret_cast<const f32x4 *>(at))
+                            : load4(at);
         x[r] = row ? (float)v[b * m.vp + (int64_t)head * m.dv + row0 + r * kTeams] : 0.0f;
     }
     const int64_t at = (int64_t)(head / m.share) * m.dk + key;
@@ -63,25 +71,50 @@ __global__ __launch_bounds__(kStepThreads) void linattn_step_kernel(
     if (m.decay == 2) gv = (float)((const T *)g)[b * m.gp + head];
     gv = gv > 0.0f ? 0.0f : gv;
     const float a = fast_exp2(gv * kLog2e);
+    float dot[kRows];
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
-        float dot = 0.0f;
+        dot[r] = 0.0f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             s[r][e] = fmaf(x[r], kv[e], a * s[r][e]);
-            dot = fmaf(s[r][e], qv[e], dot);
+            dot[r] = fmaf(s[r][e], qv[e], dot[r]);
         }
+        f32x4 *at = reinterpret_cast<f32x4 *>(hp + (int64_t)r * kTeams * m.dk);
+        if (!in || row0 + r * kTeams >= m.dv) continue;
+        if (STREAM)
+            __builtin_nontemporal_store(s[r], at);
+        else
+            *at = s[r];
+    }
+    // Sums over the team: each exchange halves the rows that a lane adds up, then a row's lanes
+    // exchange theirs.
+    int first = 0;
 #pragma unroll
-        for (int d = 1; d < TEAM; d <<= 1) dot += __shfl_xor(dot, d, 64);
-        if (row0 + r * kTeams < m.dv) {
-            if (in) *reinterpret_cast<f32x4 *>(hp + (int64_t)r * kTeams * m.dk) = s[r];
-            if (key == 0) o[bh * m.dv + row0 + r * kTeams] = Elem<T>::from_f32(dot * m.scale);
+    for (int d = 1, n = kRows; d < TEAM; d <<= 1) {
+        if (n > 1) {
+            n >>= 1;
+            const bool upper = lane & d;
+            first += upper ? n : 0;
+#pragma unroll
+            for (int r = 0; r < n; ++r) {
+                const float other = __shfl_xor(upper ? dot[r] : dot[r + n], d, 64);
+                dot[r] = (upper ? dot[r + n] : dot[r]) + other;
+            }
+        } else {
+            dot[0] += __shfl_xor(dot[0], d, 64);
         }
+    }
+    if ((lane % TEAM) >= kRows) return;        // another lane's row
+#pragma unroll
+    for (int r = 0; r < (TEAM < kRows ? kRows / TEAM : 1); ++r) {
+        const int row = row0 + (first + r) * kTeams;
+        if (row < m.dv) o[bh * m.dv + row] = Elem<T>::from_f32(dot[r] * m.scale);
     }
 }
 
-template <typename T, int TEAM>
-hipError_t step_go(const LinattnShape &s, const LinattnArgs &a, float *h, hipStream_t st)
+template <typename T, int TEAM, bool STREAM>
+hipError_t step_team(const LinattnShape &s, const LinattnArgs &a, float *h, hipStream_t st)
 {
     StepDims m;
     m.qp = s.qp; m.kp = s.kp; m.vp = s.vp; m.gp = s.gp;
@@ -92,9 +125,16 @@ hipError_t step_go(const LinattnShape &s, const LinattnArgs &a, float *h, hipStr
     m.waves = s.b * s.H * m.blocks;
     m.scale = s.scale;
     const int64_t groups = (m.waves + kStepThreads / 64 - 1) / (kStepThreads / 64);
-    hipLaunchKernelGGL((linattn_step_kernel<T, TEAM>), dim3((unsigned)groups), dim3(kStepThreads), 0, st,
+    hipLaunchKernelGGL((linattn_step_kernel<T, TEAM, STREAM>), dim3((unsigned)groups), dim3(kStepThreads), 0, st,
                        (const T *)a.q, (const T *)a.k, (const T *)a.v, a.g, h, (T *)a.o, m);
     return hipGetLastError();
+}
+
+template <typename T, int TEAM>
+hipError_t step_go(const LinattnShape &s, const LinattnArgs &a, float *h, hipStream_t st)
+{
+    return s.b * s.H * s.dv * s.dk * 4 <= kCached ? step_team<T, TEAM, false>(s, a, h, st)
+                                                  : step_team<T, TEAM, true>(s, a, h, st);
 }
 
 template <typename T>
