@@ -344,6 +344,9 @@ __global__ __launch_bounds__(kThreads, (waves_for<T, DK, NV>())) void walk_kerne
     typedef typename Tile<T>::frag Frag;
     typedef typename Raw4<T>::t Raw;
     constexpr bool kOuts = KIND != kEnds, kParts = KIND == kDq || KIND == kDk;
+    // Scores in two bf16 parts: the decays' gradient adds up their products with both sides' rows,
+    // and the error of its sums was half as large again as that of its own rounding with one.
+    constexpr bool kFine = kParts && sizeof(T) == 2;
     constexpr int CH = chunk_tokens<T, DK>(), NI = CH / 16, kTiles = NI * (NI + 1) / 2;
     constexpr int BV = 64 * NV;                                      // values
     typedef Rows<T, DK> KeyRows;
@@ -359,7 +362,7 @@ __global__ __launch_bounds__(kThreads, (waves_for<T, DK, NV>())) void walk_kerne
     __shared__ __attribute__((aligned(16))) T sK[NI * KeyRows::kTile];
     __shared__ __attribute__((aligned(16))) T sV[NI * ValRows::kTile];
     __shared__ __attribute__((aligned(16))) T sQ[NI * KeyRows::kTile];
-    __shared__ __attribute__((aligned(16))) T sP[CH * PP];
+    __shared__ __attribute__((aligned(16))) T sP[kFine ? 2 * CH * PP : CH * PP];
     __shared__ __attribute__((aligned(16))) float sHi[CH], sLo[CH], sIn[CH], sW[CH];
     __shared__ float sPart[4][CH], sWritten[4][CH], sX[4];
 
@@ -468,7 +471,7 @@ __global__ __launch_bounds__(kThreads, (waves_for<T, DK, NV>())) void walk_kerne
     };
 
     if constexpr (kOuts)      // scores across the diagonal stay zero
-        for (int i = tid; i < CH * PP; i += kThreads) sP[i] = (T)0.0f;
+        for (int i = tid; i < (int)(sizeof(sP) / sizeof(T)); i += kThreads) sP[i] = (T)0.0f;
     if (count > 0) fetch(REV ? c0 + count - 1 : c0);
 
     // Of two workgroups on a compute unit (256 apart) one goes first: in step they would both be in
@@ -573,7 +576,13 @@ __global__ __launch_bounds__(kThreads, (waves_for<T, DK, NV>())) void walk_kerne
                     }
 #pragma unroll
                 for (int r = 0; r < 4; ++r) p[r] *= a.intra * fast_exp2(e[r]);
-                store4(sP + (16 * i + c16) * PP + paired_place<T>(u, g4), p);
+                T *at = sP + (16 * i + c16) * PP + paired_place<T>(u, g4);
+                store4(at, p);
+                if constexpr (kFine) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) p[r] -= (float)(T)p[r];
+                    store4(at + CH * PP, p);
+                }
             }
 
             // what the state before the chunk gives
@@ -670,10 +679,13 @@ __global__ __launch_bounds__(kThreads, (waves_for<T, DK, NV>())) void walk_kerne
 #pragma unroll
                 for (int m = 0; m < MM; ++m) {
                     if (REV ? Tile<T>::kStep * (m + 1) <= 16 * i : Tile<T>::kStep * m > 16 * i) continue;
-                    const Frag p = *reinterpret_cast<const Frag *>(
-                        sP + (16 * i + c16) * PP + Tile<T>::kStep * m + Tile<T>::kPart * g4);
+                    const T *at = sP + (16 * i + c16) * PP + Tile<T>::kStep * m + Tile<T>::kPart * g4;
 #pragma unroll
-                    for (int v = 0; v < NV; ++v) o[v][i] = mma16(vf[m][v], p, o[v][i]);
+                    for (int e = 0; e < (kFine ? 2 : 1); ++e) {
+                        const Frag p = *reinterpret_cast<const Frag *>(at + e * CH * PP);
+#pragma unroll
+                        for (int v = 0; v < NV; ++v) o[v][i] = mma16(vf[m][v], p, o[v][i]);
+                    }
                 }
             if constexpr (kParts) {
 #pragma unroll
