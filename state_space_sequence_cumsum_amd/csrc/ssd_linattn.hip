@@ -430,14 +430,26 @@ __global__ __launch_bounds__(kThreads, (waves_for<T, DK, NV>())) void walk_kerne
     uint32_t qoff = kcol < a.kd ? bytes(krow, a.qp, kcol) : kNowhere;
     uint32_t voff = vcol < vw ? bytes(vrow, a.vp, vcol) : kNowhere;
     const uint32_t goff = bytes(lane, a.gp, h);
-    const auto fetch = [&](int c) {
-        const int t0 = c * CH, rows = min(CH, n - t0);
-        const rsrc_t rk = rows_at(kb, a.kp, t0, rows, a.kd), rv = rows_at(vbp, a.vp, t0, rows, vw);
-        asm volatile("" : "+v"(koff), "+v"(qoff), "+v"(voff));      // (as the places in LDS below)
+    // A chunk's rows are asked for in three goes between products: a load waits for room among those
+    // on their way, and one after the other the twelve of a chunk held their wave up for 4000
+    // to 5500 cycles with the chip full.
+    const auto fetch_k = [&](int c) {
+        const int t0 = c * CH;
+        const rsrc_t rk = rows_at(kb, a.kp, t0, min(CH, n - t0), a.kd);
+        asm volatile("" : "+v"(koff), "+v"(voff), "+v"(qoff));      // (as the places in LDS below)
 #pragma unroll
         for (int i = 0; i < KI; ++i) kr[i] = buf_load_b128(rk, koff + bytes(i * KR, a.kp, 0));
+    };
+    const auto fetch_v = [&](int c) {
+        const int t0 = c * CH;
+        const rsrc_t rv = rows_at(vbp, a.vp, t0, min(CH, n - t0), vw);
+        asm volatile("" : "+v"(koff), "+v"(voff), "+v"(qoff));
 #pragma unroll
         for (int i = 0; i < VI; ++i) vr[i] = buf_load_b128(rv, voff + bytes(i * VR, a.vp, 0));
+    };
+    const auto fetch_q = [&](int c) {
+        const int t0 = c * CH, rows = min(CH, n - t0);
+        asm volatile("" : "+v"(koff), "+v"(voff), "+v"(qoff));
         if constexpr (kOuts) {
             const rsrc_t rq = rows_at(qb, a.qp, t0, rows, a.kd);
 #pragma unroll
@@ -472,7 +484,12 @@ __global__ __launch_bounds__(kThreads, (waves_for<T, DK, NV>())) void walk_kerne
 
     if constexpr (kOuts)      // scores across the diagonal stay zero
         for (int i = tid; i < (int)(sizeof(sP) / sizeof(T)); i += kThreads) sP[i] = (T)0.0f;
-    if (count > 0) fetch(REV ? c0 + count - 1 : c0);
+    if (count > 0) {
+        const int first = REV ? c0 + count - 1 : c0;
+        fetch_k(first);
+        fetch_v(first);
+        fetch_q(first);
+    }
 
     // Of two workgroups on a compute unit (256 apart) one goes first: in step they would both be in
     // products, or both in what lies between (out: 77 us against 81 with 16384 tokens of 16 heads
@@ -632,10 +649,12 @@ __global__ __launch_bounds__(kThreads, (waves_for<T, DK, NV>())) void walk_kerne
             }
         }
 
-        // the chunk ahead is asked for here, so that its rows hold no registers while the products
-        // above need them
+        // the chunk ahead is asked for from here on, so that its rows hold no registers while the
+        // products above need them
+        const bool more = it + 1 < count;
+        const int ahead = REV ? c - 1 : c + 1;
         __builtin_amdgcn_sched_barrier(0);
-        if (it + 1 < count) fetch(REV ? c - 1 : c + 1);
+        if (more) fetch_k(ahead);
 
         // the state behind the chunk
         Frag vf[MM][NV];
@@ -668,6 +687,11 @@ __global__ __launch_bounds__(kThreads, (waves_for<T, DK, NV>())) void walk_kerne
 #pragma unroll
                         for (int v = 0; v < NV; ++v) S[v][kt + i] = mma16(k[i], w[v][e], S[v][kt + i]);
             }
+            static_assert(MM > 1, "");
+            __builtin_amdgcn_sched_barrier(0);
+            if (more && m == 0) fetch_v(ahead);
+            if (more && m == 1) fetch_q(ahead);
+            __builtin_amdgcn_sched_barrier(0);
         }
         if (!kOuts) __builtin_amdgcn_s_setprio(0);
         __syncthreads();
@@ -763,27 +787,38 @@ __global__ __launch_bounds__(kThreads, (waves_for<T, DK, NV>())) void walk_kerne
 
 // ---------------------------------------------------------------------------
 // Starts of the segments of every head out of their ends, in place, and the last state: a thread
-// for four elements of a head's state, eight segments' ends on their way at a time.
+// for four elements of a head's state, the next kAhead segments' ends on their way while those
+// before them are chained.  One wave a workgroup, as a single head has no more than 64 to spread.
 // ---------------------------------------------------------------------------
-__global__ __launch_bounds__(kThreads) void chain_kernel(float *ends, const float *__restrict__ decays,
-                                                         const float *init, float *last, int64_t quads,
-                                                         int size4, int nseg)
+constexpr int kChainThreads = 64;
+__global__ __launch_bounds__(kChainThreads) void chain_kernel(float *ends, const float *__restrict__ decays,
+                                                              const float *init, float *last, int64_t quads,
+                                                              int size4, int nseg)
 {
     constexpr int kAhead = 8;
-    const int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    const int64_t id = (int64_t)blockIdx.x * kChainThreads + threadIdx.x;
     if (id >= quads) return;
     const int64_t bh = id / size4;
     f32x4 *p = reinterpret_cast<f32x4 *>(ends) + bh * nseg * size4 + id % size4;
     f32x4 S = init ? reinterpret_cast<const f32x4 *>(init)[id] : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int s0 = 0; s0 < nseg; s0 += kAhead) {
-        f32x4 end[kAhead];
-        float d[kAhead];
+    f32x4 end[kAhead], next[kAhead];
+    float d[kAhead], dnext[kAhead];
+    const auto fetch = [&](int s0) {
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
             const int s = min(s0 + i, nseg - 1);
-            end[i] = p[(int64_t)s * size4];
-            d[i] = decays[bh * nseg + s];
+            next[i] = p[(int64_t)s * size4];
+            dnext[i] = decays[bh * nseg + s];
         }
+    };
+    fetch(0);
+    for (int s0 = 0; s0 < nseg; s0 += kAhead) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            end[i] = next[i];
+            d[i] = dnext[i];
+        }
+        if (s0 + kAhead < nseg) fetch(s0 + kAhead);
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
             if (s0 + i >= nseg) break;
@@ -917,8 +952,8 @@ template <typename T, bool REV> hipError_t starts_go(const Walk &a, float *last,
     if (e != hipSuccess) return e;
     const int size4 = a.kd * a.vd / 4;
     const int64_t quads = bh * size4;
-    hipLaunchKernelGGL(chain_kernel, dim3((unsigned)((quads + kThreads - 1) / kThreads)), dim3(kThreads), 0,
-                       st, a.ends, a.decays, a.init, last, quads, size4, a.nseg);
+    hipLaunchKernelGGL(chain_kernel, dim3((unsigned)((quads + kChainThreads - 1) / kChainThreads)),
+                       dim3(kChainThreads), 0, st, a.ends, a.decays, a.init, last, quads, size4, a.nseg);
     return hipGetLastError();
 }
 
