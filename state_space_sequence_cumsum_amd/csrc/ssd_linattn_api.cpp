@@ -53,6 +53,14 @@ ssd::LinattnShape linattn_shape(const ssd_linattn_problem *p)
     return s;
 }
 
+// Decays and lengths are read element by element.
+bool decays_aligned(const ssd_linattn_problem *p, const void *g, const void *dg, const int32_t *lengths)
+{
+    const bool own = p->decay == SSD_DECAY_NONE ||
+                     on_bytes(p->decay == SSD_DECAY_HEAD ? 4 : bytes_of(p->dtype), {g});
+    return own && on_bytes(bytes_of(p->dtype), {dg}) && on_bytes(4, {lengths});
+}
+
 // Rows are read 16 bytes at a time.
 bool rows_aligned(const ssd_linattn_problem *p, std::initializer_list<int64_t> pitches)
 {
@@ -124,6 +132,7 @@ ssd_status ssd_linattn(const ssd_linattn_problem *problem, const void *q, const 
     const bool work = need > SSD_LINATTN_NO_WORKSPACE;
     if (work && (workspace == nullptr || workspace_bytes < need)) return SSD_ERR_WORKSPACE;
     if (!on_bytes(16, {q, k, v, o, h0, hT, work ? workspace : nullptr}) ||
+        !decays_aligned(problem, g, nullptr, lengths) ||
         !rows_aligned(problem, {problem->q_pitch, problem->k_pitch, problem->v_pitch}))
         return SSD_ERR_MISALIGNED;
     const Inputs in = inputs_of(problem, q, k, v, g);
@@ -160,6 +169,7 @@ ssd_status ssd_linattn_backward(const ssd_linattn_problem *problem, const void *
     const bool work = need > SSD_LINATTN_NO_WORKSPACE;
     if (work && (workspace == nullptr || workspace_bytes < need)) return SSD_ERR_WORKSPACE;
     if (!on_bytes(16, {dout, q, k, v, h0, dhT, dq, dk, dv, dh0, work ? workspace : nullptr}) ||
+        !decays_aligned(problem, g, dg, lengths) ||
         !rows_aligned(problem, {p.q_pitch, p.k_pitch, p.v_pitch, p.do_pitch}))
         return SSD_ERR_MISALIGNED;
     const int64_t e = bytes_of(p.dtype), rows = p.batch * p.seqlen;
@@ -183,7 +193,7 @@ ssd_status ssd_linattn_step(const ssd_linattn_problem *problem, const void *q, c
     if (st != SSD_OK) return st;
     if (problem->seqlen != 1) return SSD_ERR_BAD_SHAPE;
     if (!q || !k || !v || !h || !o || (!g && problem->decay != SSD_DECAY_NONE)) return SSD_ERR_NULL_ARG;
-    if (!on_bytes(16, {q, k, v, o, h}) ||
+    if (!on_bytes(16, {q, k, v, o, h}) || !decays_aligned(problem, g, nullptr, nullptr) ||
         !rows_aligned(problem, {problem->q_pitch, problem->k_pitch, problem->v_pitch}))
         return SSD_ERR_MISALIGNED;
     Inputs in = inputs_of(problem, q, k, v, g);

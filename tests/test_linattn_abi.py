@@ -157,6 +157,25 @@ def test_linattn_pointer_checks():
     assert binding.lib().ssd_last_hip_error() == 0
 
 
+def test_decays_and_lengths_on_their_own_sizes():
+    L, odd = linattn.lib(), ctypes.c_void_p(OK16.value + 2 + 1)
+    for decay, dtype in ((1, 1), (2, 0), (2, 1)):
+        kw = dict(decay=decay, dtype=dtype)
+        for at in (3, 5):                            # g, lengths
+            a = [OK16] * 9
+            a[at] = odd
+            assert L.ssd_linattn(ctypes.byref(_problem(**kw)), *a, 1 << 50, None) == 6
+        a = [OK16] * 6
+        a[3] = odd
+        assert L.ssd_linattn_step(ctypes.byref(_problem(seqlen=1, **kw)), *a, None) == 6
+        for at in (4, 7) + ((11,) if decay == 2 else ()):
+            a = [OK16] * 14
+            a[at] = odd
+            if decay != 2:
+                a[11] = None
+            assert L.ssd_linattn_backward(ctypes.byref(_problem(**kw)), *a, 1 << 50, None) == 6
+
+
 def _far(n):
     return [(i + 1) << 40 for i in range(n)]
 
