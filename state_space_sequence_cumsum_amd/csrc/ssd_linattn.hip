@@ -71,7 +71,9 @@ struct Walk {
     int64_t groups;             // heads x segments
     // kDq, kDk: the array whose products with the outputs the decays' gradient takes (q, k): those
     // (kDk: of what the chunk's own tokens give, and of what the state behind it gives), and the states
-    // before each chunk, [b H, chunks, vd, kd], with their products with the gradients behind it
+    // before each chunk, [b H, chunks, nvb] of them as a workgroup's lanes hold them (both walks have
+    // the same roles of values and keys): whole 16-byte accesses, lane beside lane, with their
+    // products with the gradients behind it
     const void *x;
     int64_t xp;
     int xdiv;
@@ -536,18 +538,17 @@ __global__ __launch_bounds__(kThreads, (waves_for<T, DK, NV>())) void walk_kerne
         // the states before the chunk, out of the forward walk for the backward one, which asks for
         // them early where registers allow
         constexpr bool kAhead = KIND == kDk && sizeof(T) == 2;
-        Raw before[kAhead ? NV : 1][kAhead ? KT : 1];
-        const rsrc_t rs = make_rsrc(kParts ? (T *)a.states + (bh * a.nchunks + c) * size : nullptr,
-                                    (int)(size * sizeof(T)));
-        const auto state_off = [&](int v, int kt) {
-            const int key = 16 * kt + 4 * g4, val = val0 + 16 * v;
-            return val < vw && key < a.kd ? (uint32_t)(((v0 + val) * a.kd + key) * (int)sizeof(T)) : ~0u;
-        };
+        constexpr int KP = KT * (int)sizeof(T) / 4;        // 16-byte pieces of a lane's keys
+        u32x4 before[kAhead ? NV : 1][kAhead ? KP : 1];
+        const rsrc_t rs = make_rsrc(
+            kParts ? (T *)a.states + ((bh * a.nchunks + c) * a.nvb + vb) * (BV * DK) : nullptr,
+            BV * DK * (int)sizeof(T));
+        const auto piece = [&](int v, int kp) { return (uint32_t)(((wave * NV + v) * KP + kp) * 64 + lane) * 16; };
         if constexpr (kAhead)
 #pragma unroll
             for (int v = 0; v < NV; ++v)
 #pragma unroll
-                for (int kt = 0; kt < KT; ++kt) before[v][kt] = buf_load4(rs, state_off(v, kt), (T *)nullptr);
+                for (int kp = 0; kp < KP; ++kp) before[v][kp] = buf_load_b128(rs, piece(v, kp));
         if constexpr (kOuts) {
             if constexpr (kParts) {
                 // rows whose products with the outputs the decays' gradient takes
@@ -638,10 +639,20 @@ __global__ __launch_bounds__(kThreads, (waves_for<T, DK, NV>())) void walk_kerne
 #pragma unroll
             for (int v = 0; v < NV; ++v)
 #pragma unroll
-                for (int kt = 0; kt < KT; ++kt) {
-                    if constexpr (KIND == kDq) buf_store4(rs, state_off(v, kt), S[v][kt], (T *)nullptr);
-                    else if constexpr (kAhead) x += dot4(as_floats(before[v][kt]), S[v][kt]);
-                    else x += dot4(as_floats(buf_load4(rs, state_off(v, kt), (T *)nullptr)), S[v][kt]);
+                for (int kp = 0; kp < KP; ++kp) {
+                    if constexpr (KIND == kDq) {
+                        buf_store_b128(rs, piece(v, kp), __builtin_bit_cast(u32x4, of_accumulators<T>(S[v], kp)));
+                    } else {
+                        u32x4 w;
+                        if constexpr (kAhead) w = before[v][kp];
+                        else w = buf_load_b128(rs, piece(v, kp));
+                        if constexpr (sizeof(T) == 4) {
+                            x += dot4(as_floats(w), S[v][kp]);
+                        } else {
+                            x += dot4(as_floats(u2{w[0], w[1]}), S[v][2 * kp]);
+                            x += dot4(as_floats(u2{w[2], w[3]}), S[v][2 * kp + 1]);
+                        }
+                    }
                 }
             if constexpr (KIND == kDk) {
                 x = rows_sum(columns_sum(x)) * whole;
@@ -988,6 +999,9 @@ int part_chunks(const LinattnShape &s)
     return (int)((s.L + n - 1) / n);
 }
 
+// Keys that a walk's state has room for.
+int64_t padded_keys(int64_t keys) { return keys <= 64 ? 64 : keys <= 128 ? 128 : 256; }
+
 // Workspace of one split: ends and decays (byte offsets).
 int64_t ends_bytes(const LinattnShape &s, int nseg)
 {
@@ -1024,7 +1038,7 @@ GradLayout grad_layout(const LinattnShape &s, bool gates)
         return off;
     };
     const int64_t bh = s.b * s.H, nvb = blocks_of(s.bf16, kDq, s.dk), nc = part_chunks(s);
-    y.states = take(gates, bh * nc * s.dk * s.dv * (s.bf16 ? 2 : 4));
+    y.states = take(gates, bh * nc * nvb * 64 * padded_keys(s.dv) * (s.bf16 ? 2 : 4));
     y.read = take(gates, bh * nvb * s.L * 4);
     y.own = take(gates, bh * nvb * s.L * 4);
     y.written = take(gates, bh * nvb * s.L * 4);
