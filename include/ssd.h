@@ -453,10 +453,13 @@ ssd_status ssd_norm(const ssd_norm_problem *problem, const void *x, const void *
  *   - q, k, v, do and their rows start on 16 bytes (pitches are multiples of 16 bytes), as do
  *     outputs, states and the workspace; else SSD_ERR_MISALIGNED.
  *   - states and sums are fp32.  For SSD_BF16 the decayed scores and the state that a chunk of
- *     64 tokens reads are rounded to bf16 for the matrix products; what is added to a state
- *     is not, so that states have fp32's precision.
- *   - tokens go through in chunks of 64: a value that is not finite in q, k, v or do may make
- *     NaN of any output of its chunk, not only of those that the recurrence leads to.
+ *     64 tokens reads are rounded to bf16 for the matrix products; what is added to a state that
+ *     is handed out is not, so that states have fp32's precision.
+ *   - tokens go through in chunks of 64 (32 of fp32 keys wider than 128): a value that is not finite in
+ *     q, k, v, do or a state may make NaN of any output of its chunk and of those behind it (in
+ *     gradients: before it), not only of those that the recurrence leads to.
+ *   - g, its gradient and lengths lie on their own element's size, else SSD_ERR_MISALIGNED.
+ *   - calls that may run at once need workspaces of their own; so do captured graphs.
  * ------------------------------------------------------------------------- */
 typedef enum { SSD_DECAY_NONE = 0, SSD_DECAY_HEAD = 1, SSD_DECAY_TOKEN = 2 } ssd_decay;
 

@@ -22,9 +22,23 @@
 // in fp32, those of the rest err by less than 2^-27, however far G has fallen.
 //
 // Rounding.  States and all sums are fp32.  For bf16 the matrix operands are bf16: inputs as
-// they are, the decayed scores and the state that a chunk reads each rounded once; but what
-// is added to the state, w_s v_s, goes in as three bf16 parts (8 + 8 + 8 bits, fp32's 24), so
-// that states, which leave the kernel in fp32, hold fp32's precision.
+// they are, the decayed scores and the state that a chunk reads each rounded once (twice the half
+// step of an output's own rounding at most; two parts of each with a gradient of the decays); but
+// what is added to the state, w_s v_s, goes in as three bf16 parts (8 + 8 + 8 bits, fp32's 24)
+// where the state leaves the kernel in fp32 or starts a segment, and as two where it only makes the
+// outputs of its own segment, an error of 2^-17.
+//
+// Segments.  A walk is serial, 4 us a chunk of 64 tokens, and a chip full of walks takes 512
+// workgroups.  Where heads and blocks of values give fewer, a first walk without outputs leaves the
+// ends of segments of the prompt, from zero, a chain turns them into starts, and the outputs' walk
+// takes all segments at once: 16384 tokens of 16 heads of 128 x 128 in 512 workgroups take 125 us (38
+// + 16 + 66, launches apart; 22 us would be the 134 GFLOP of the products at a large product's rate, 44
+// the bytes at a copy's), in 16 walks of one wave's chain of 256 chunks 1.1 ms.
+//
+// What bounds it: a chunk is a chain of short phases between two barriers (rows to LDS, scores,
+// state read, state update, outputs), 9000 to 12000 cycles with two workgroups a CU, of which the
+// matrix instructions take a fifth and neither HBM (a third) nor LDS is full; asking for the
+// next chunk's rows is the longest (its loads wait for room), then the state update.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -213,6 +227,18 @@ __device__ __forceinline__ typename Tile<T>::frag of_accumulators(const f32x4 (&
         return __builtin_bit_cast(bf16x8, r);
     }
 }
+// What bf16 leaves of those accumulators, as an operand.
+template <int N> __device__ __forceinline__ bf16x8 rest_of_accumulators(const f32x4 (&acc)[N], int m, const bf16x8 &part)
+{
+    const u32x4 w = __builtin_bit_cast(u32x4, part);
+    u32x4 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const f32x4 &x = acc[2 * m + (i >> 1)];
+        r[i] = pack_bf16(x[2 * (i & 1)] - bf_lo(w[i]), x[2 * (i & 1) + 1] - bf_hi(w[i]));
+    }
+    return __builtin_bit_cast(bf16x8, r);
+}
 // Where source `s` of a target's scores is kept, for a paired read of 16 bytes.
 template <typename T> __device__ __forceinline__ int paired_place(int tile, int g4)
 {
@@ -346,8 +372,9 @@ __global__ __launch_bounds__(kThreads, (waves_for<T, DK, NV>())) void walk_kerne
     typedef typename Tile<T>::frag Frag;
     typedef typename Raw4<T>::t Raw;
     constexpr bool kOuts = KIND != kEnds, kParts = KIND == kDq || KIND == kDk;
-    // Scores in two bf16 parts: the decays' gradient adds up their products with both sides' rows,
-    // and the error of its sums was half as large again as that of its own rounding with one.
+    // Scores and the state that is read in two bf16 parts: the decays' gradient adds up their
+    // products with both sides' rows, and with one part its error, 2.6e-3 of its size, was half as
+    // large again as that of its own rounding (1.7e-3; now below 2.3e-3).  2 % of the gradients' time.
     constexpr bool kFine = kParts && sizeof(T) == 2;
     constexpr int CH = chunk_tokens<T, DK>(), NI = CH / 16, kTiles = NI * (NI + 1) / 2;
     constexpr int BV = 64 * NV;                                      // values
@@ -615,6 +642,11 @@ __global__ __launch_bounds__(kThreads, (waves_for<T, DK, NV>())) void walk_kerne
                     const Frag f = of_accumulators<T>(S[v], kk);
 #pragma unroll
                     for (int i = 0; i < NI; ++i) o[v][i] = mma16(f, q[i], o[v][i]);
+                    if constexpr (kFine) {
+                        const Frag r = rest_of_accumulators(S[v], kk, f);
+#pragma unroll
+                        for (int i = 0; i < NI; ++i) o[v][i] = mma16(r, q[i], o[v][i]);
+                    }
                 }
             }
 #pragma unroll
