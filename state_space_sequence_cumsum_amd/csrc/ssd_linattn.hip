@@ -31,14 +31,15 @@
 // Segments.  A walk is serial, 4 us a chunk of 64 tokens, and a chip full of walks takes 512
 // workgroups.  Where heads and blocks of values give fewer, a first walk without outputs leaves the
 // ends of segments of the prompt, from zero, a chain turns them into starts, and the outputs' walk
-// takes all segments at once: 16384 tokens of 16 heads of 128 x 128 in 512 workgroups take 125 us (38
-// + 16 + 66, launches apart; 22 us would be the 134 GFLOP of the products at a large product's rate, 44
-// the bytes at a copy's), in 16 walks of one wave's chain of 256 chunks 1.1 ms.
+// takes all segments at once: 16384 tokens of 16 heads of 128 x 128 take 125 us in 512 workgroups
+// (ends 38, chain 16, outputs 66; the 271 MB of inputs and outputs at a copy's rate would take 44, the
+// 17 GFLOP of a token's 4 x 128 x 128 at a large product's 15), and 1 ms in 16 walks of 256 chunks each.
 //
 // What bounds it: a chunk is a chain of short phases between two barriers (rows to LDS, scores,
 // state read, state update, outputs), 9000 to 12000 cycles with two workgroups a CU, of which the
-// matrix instructions take a fifth and neither HBM (a third) nor LDS is full; asking for the
-// next chunk's rows is the longest (its loads wait for room), then the state update.
+// matrix instructions take a fifth, and HBM is busy less than half of the time (2.7 TB/s in the
+// outputs' walk); asking for the next chunk's rows is the longest (its loads wait for room), then
+// the state update.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
