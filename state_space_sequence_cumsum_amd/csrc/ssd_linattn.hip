@@ -1209,7 +1209,8 @@ hipError_t backward_go(const LinattnShape &s, const LinattnGradArgs &a, hipStrea
         const int64_t quads = s.b * s.L * s.G * (s.dk / 4);
         for (int i = 0; i < 2; ++i) {
             hipLaunchKernelGGL((shared_sum_kernel<T>), dim3(groups_for(quads, kThreads)), dim3(kThreads),
-                               0, st, (const float *)at(i ? y.dk : y.dq), (T *)(i ? a.dk : a.dq), a.lengths, quads, (int)s.L, (int)s.G, share, (int)s.dk);
+                               0, st, (const float *)at(i ? y.dk : y.dq), (T *)(i ? a.dk : a.dq),
+                               a.lengths, quads, (int)s.L, (int)s.G, share, (int)s.dk);
             e = hipGetLastError();
             if (e != hipSuccess) return e;
         }

@@ -274,19 +274,20 @@ def ssd_rotary(q, k, freqs, positions=None, *, interleaved=False, inverse=False,
     does.  Outputs may be q and k themselves where those are contiguous.  Returns q_out, or
     (q_out, k_out) with a k."""
     code, dev = _io(q, "q")
-    td = q.dtype
-    if q.dim() not in (3, 4):
+    td, shape = q.dtype, q.shape
+    lead = len(shape) - 2
+    if lead not in (1, 2):
         raise ValueError("ssd_rotary takes q [b, L, heads, width] or [b, heads, width]")
-    lead = q.dim() - 2
-    tokens, (hq, width) = tuple(q.shape[:lead]), q.shape[lead:]
-    b, L = tokens[0], tokens[1] if lead == 2 else 1
-    qp, q_pitch = _rows(q, "q", td, q.shape, dev, lead)
-    kp, k_pitch, hk = None, 0, 0
+    b, hq, width = shape[0], shape[-2], shape[-1]
+    L = shape[1] if lead == 2 else 1
+    qp, q_pitch = _rows(q, "q", td, shape, dev, lead)
+    kp, k_pitch, hk, k_shape = None, 0, 0, None
     if k is not None:
-        if not isinstance(k, Tensor) or k.dim() != q.dim():
+        if not isinstance(k, Tensor) or k.dim() != lead + 2:
             raise ValueError("k must be a GPU tensor with q's dimensions")
         hk = k.shape[lead]
-        kp, k_pitch = _rows(k, "k", td, (*tokens, hk, width), dev, lead)
+        k_shape = (b, L, hk, width) if lead == 2 else (b, hk, width)
+        kp, k_pitch = _rows(k, "k", td, k_shape, dev, lead)
         if hk == 0:
             raise ValueError("k has no heads: give None")
     elif k_out is not None:
@@ -297,16 +298,22 @@ def ssd_rotary(q, k, freqs, positions=None, *, interleaved=False, inverse=False,
     pp, mode = None, POSITIONS_START
     if positions is not None:
         each = lead == 2 and isinstance(positions, Tensor) and positions.dim() == 2
-        pp = _dense(positions, "positions", torch.int32, tokens if each else (b,), dev)
+        pp = _dense(positions, "positions", torch.int32, (b, L) if each else (b,), dev)
         mode = POSITIONS_EACH if each else POSITIONS_FIRST
-    outs, ops = [], []
-    for x, y, name in ((q, q_out, "q_out"), (k, k_out, "k_out")):
-        if x is not None and y is None:
-            y = _empty(x.shape, td, x.device, stream)
-        outs.append(y)
-        ops.append(None if x is None else _dense(y, name, td, x.shape, dev))
+    if q_out is None:
+        q_out = _empty(shape, td, q.device, stream)
+        oq = q_out.data_ptr()
+    else:
+        oq = _dense(q_out, "q_out", td, shape, dev)
+    ok = None
+    if k is not None:
+        if k_out is None:
+            k_out = _empty(k_shape, td, q.device, stream)
+            ok = k_out.data_ptr()
+        else:
+            ok = _dense(k_out, "k_out", td, k_shape, dev)
     prob = RotaryProblem(b, L, hq, hk, width, 2 * freqs.shape[0], q_pitch, k_pitch, scale, mode,
                          1 if interleaved else 0, 1 if inverse else 0, code)
-    _call(lib().ssd_rotary, (ctypes.byref(prob), qp, kp, fp, pp, *ops, _stream(stream, dev)), dev,
+    _call(lib().ssd_rotary, (ctypes.byref(prob), qp, kp, fp, pp, oq, ok, _stream(stream, dev)), dev,
           "ssd_rotary")
-    return outs[0] if k is None else tuple(outs)
+    return q_out if k is None else (q_out, k_out)
