@@ -489,7 +489,21 @@ __global__ __launch_bounds__(kThreads, (waves_for<T, DK, NV>())) void walk_kerne
         if (a.decay == SSD_DECAY_TOKEN)
             gn = buf_load1(rows_at((const T *)a.g + row0 * a.gp, a.gp, t0, rows, a.H), goff, (T *)nullptr);
     };
-    // the decays' gradient: a chunk's parts of the waves, added up behind a barrier
+    // The decays' gradient: a chunk's parts of the waves, added up by the first one.  What the waves put
+    // down between the chunk's two barriers is gathered behind the second one, into the first
+    // wave's own place, as they put down the next chunk's behind the next barrier; what they put
+    // down behind the second one is added up, and all of it stored, behind the next barrier.
+    const auto gather_parts = [&] {
+        if (wave != 0 || lane >= CH) return;
+        float written = 0.0f, cross = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            written += sWritten[w][lane];
+            cross += sX[w];
+        }
+        sWritten[0][lane] = written;
+        if (lane == 0) sX[0] = cross;
+    };
     const auto store_parts = [&](int c) {
         const int t = c * CH + lane;
         if (wave != 0 || lane >= CH || t >= n) return;
@@ -500,15 +514,10 @@ __global__ __launch_bounds__(kThreads, (waves_for<T, DK, NV>())) void walk_kerne
         if constexpr (KIND == kDq) {
             a.part[at] = part;
         } else {
-            float written = 0.0f, cross = 0.0f;
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                written += sWritten[w][lane];
-                cross += sX[w];
-            }
+            const float written = sWritten[0][lane];
             a.part[at] = part - written;
             a.written[at] = written;
-            if (lane == 0) a.cross[(bh * a.nvb + vb) * a.nchunks + c] = cross;
+            if (lane == 0) a.cross[(bh * a.nvb + vb) * a.nchunks + c] = sX[0];
         }
     };
 
@@ -739,6 +748,7 @@ __global__ __launch_bounds__(kThreads, (waves_for<T, DK, NV>())) void walk_kerne
         }
         if (!kOuts) __builtin_amdgcn_s_setprio(0);
         __syncthreads();
+        if constexpr (KIND == kDk) gather_parts();
 
         if constexpr (kOuts) {
             // what the chunk's own tokens give: steps of sources that reach these targets
