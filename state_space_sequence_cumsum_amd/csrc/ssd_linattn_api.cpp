@@ -37,6 +37,14 @@ ssd_status check_linattn(const ssd_linattn_problem *p)
     return tokens_fit(p->batch, p->seqlen) ? SSD_OK : SSD_ERR_UNSUPPORTED;
 }
 
+// A gradient of shared queries and keys goes through rows of every head's: nheads * key_dim.
+ssd_status check_linattn_gradient(const ssd_linattn_problem *p)
+{
+    const ssd_status st = check_linattn(p);
+    if (st != SSD_OK) return st;
+    return p->nheads * p->key_dim <= kMaxRow ? SSD_OK : SSD_ERR_UNSUPPORTED;
+}
+
 ssd::LinattnShape linattn_shape(const ssd_linattn_problem *p)
 {
     ssd::LinattnShape s;
@@ -149,8 +157,9 @@ ssd_status ssd_linattn(const ssd_linattn_problem *problem, const void *q, const 
 
 size_t ssd_linattn_backward_workspace_bytes(const ssd_linattn_problem *problem)
 {
-    return check_linattn(problem) == SSD_OK ? ssd::linattn_backward_workspace_bytes(linattn_shape(problem))
-                                            : 0;
+    return check_linattn_gradient(problem) == SSD_OK
+               ? ssd::linattn_backward_workspace_bytes(linattn_shape(problem))
+               : 0;
 }
 
 ssd_status ssd_linattn_backward(const ssd_linattn_problem *problem, const void *dout, const void *q,
@@ -159,7 +168,7 @@ ssd_status ssd_linattn_backward(const ssd_linattn_problem *problem, const void *
                                 void *dv, void *dg, float *dh0, void *workspace,
                                 size_t workspace_bytes, void *stream)
 {
-    ssd_status st = check_linattn(problem);
+    ssd_status st = check_linattn_gradient(problem);
     if (st != SSD_OK) return st;
     const ssd_linattn_problem &p = *problem;
     if (!dout || !q || !k || !v || !dq || !dk || !dv || (!g && p.decay != SSD_DECAY_NONE))

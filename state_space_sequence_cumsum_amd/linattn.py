@@ -15,7 +15,6 @@ import torch
 from torch import Tensor
 
 from . import block
-from .binding import _raise
 from .block import NO_WORKSPACE, _Bound, _call, _dense, _empty, _io, _rows, _stream
 
 DECAY_NONE, DECAY_HEAD, DECAY_TOKEN = 0, 1, 2
@@ -98,19 +97,17 @@ def ssd_linattn_workspace_bytes(problem: LinattnProblem) -> int:
 
 
 def ssd_linattn_backward_workspace_bytes(problem: LinattnProblem) -> int:
-    """Bytes of workspace ssd_linattn_backward needs (1: none); 0 when the problem is not valid."""
+    """Bytes of workspace ssd_linattn_backward needs (1: none); 0 when it does not take the problem."""
     return lib().ssd_linattn_backward_workspace_bytes(ctypes.byref(problem))
 
 
-def _workspace(workspace, need, validate, problem, dev, device, stream, what):
-    """(workspace tensor or None, its address, its bytes) for `need` bytes."""
+def _workspace(workspace, need, dev, device, stream):
+    """(workspace tensor or None, its address, its bytes) for `need` bytes; 0: the call is refused."""
     if workspace is not None:
         if not (isinstance(workspace, Tensor) and workspace.get_device() == dev
                 and workspace.is_contiguous()):
             raise ValueError("workspace must be a contiguous tensor on the inputs' device")
         return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    if need == 0:
-        _raise(validate(problem), what)
     if need <= NO_WORKSPACE:
         return None, None, need
     workspace = _empty(need, torch.uint8, device, stream)
@@ -146,8 +143,7 @@ def ssd_linattn(q, k, v, g=None, h0=None, *, scale=1.0, lengths=None, o=None, hT
         tp = _dense(hT, "hT", torch.float32, states, dev)
     L, p = lib(), ctypes.byref(prob)
     need = L.ssd_linattn_workspace_bytes(p) if workspace is None else 0
-    workspace, wp, n = _workspace(workspace, need, L.ssd_linattn_validate, p, dev, device, stream,
-                                  "ssd_linattn")
+    workspace, wp, n = _workspace(workspace, need, dev, device, stream)
     _call(L.ssd_linattn, (p, *ptrs, hp, lp, op, tp, wp, n, _stream(stream, dev)), dev, "ssd_linattn")
     return o, hT
 
@@ -157,7 +153,7 @@ def ssd_linattn_backward(do, q, k, v, g=None, h0=None, dhT=None, *, scale=1.0, l
                          workspace=None, stream=None):
     """Gradients of ssd_linattn's inputs from ``do`` [b, L, heads, value], that of its o (may be
     a column slice), and ``dhT``, that of its hT (None: zeros).  The other inputs are the forward
-    call's; its outputs are not needed.
+    call's; its outputs are not needed.  heads * key may be 2^22 at most.
 
     Returns (dq, dk, dv, dg, dh0), each of its input's shape and type: dg None without a per-token
     g (fixed decays have no gradient here) or with want_dg False, dh0 None without an h0 or
@@ -183,8 +179,7 @@ def ssd_linattn_backward(do, q, k, v, g=None, h0=None, dhT=None, *, scale=1.0, l
         outs.append(t)
     L, p = lib(), ctypes.byref(prob)
     need = L.ssd_linattn_backward_workspace_bytes(p) if workspace is None else 0
-    workspace, wp, n = _workspace(workspace, need, L.ssd_linattn_validate, p, dev, device, stream,
-                                  "ssd_linattn_backward")
+    workspace, wp, n = _workspace(workspace, need, dev, device, stream)
     _call(L.ssd_linattn_backward,
           (p, dp, *ptrs, hp, tp, lp, *[None if t is None else t.data_ptr() for t in outs], wp, n,
            _stream(stream, dev)), dev, "ssd_linattn_backward")
