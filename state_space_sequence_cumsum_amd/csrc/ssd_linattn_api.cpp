@@ -149,7 +149,10 @@ ssd_status ssd_linattn(const ssd_linattn_problem *problem, const void *q, const 
                                   bytes_of(problem->dtype));
     const Area last = dense(hT, states), len = dense(lengths, problem->batch * 4);
     const Area ws = dense(work ? workspace : nullptr, (int64_t)need);
-    st = check_apart({out, last, ws}, {in.q, in.k, in.v, in.g, len, dense(h0, states, true)});
+    st = check_apart({out, last, ws}, {in.q, in.k, in.v, in.g, len});
+    // each element of a state is read before the same thread writes it
+    if (st == SSD_OK) st = check_apart({out, ws}, {dense(h0, states)});
+    if (st == SSD_OK) st = check_apart({last}, {dense(h0, states, true)});
     if (st != SSD_OK) return st;
     const ssd::LinattnArgs a = {q, k, v, g, h0, lengths, o, hT, workspace};
     return status_of(ssd::launch_linattn(linattn_shape(problem), a, (hipStream_t)stream));

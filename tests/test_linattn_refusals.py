@@ -39,3 +39,15 @@ def test_gradient_rows_of_all_heads(kw, fits):
         if p.decay != 2:
             a[11] = None
         assert L.ssd_linattn_backward(ctypes.byref(p), *a, 1 << 50, None) == 3
+
+
+@pytest.mark.parametrize("kw", [
+    dict(seqlen=100), dict(seqlen=128), dict(seqlen=128, nheads=16, value_dim=64), dict(seqlen=64, dtype=0),
+    dict(seqlen=144, key_dim=72), dict(seqlen=72, key_dim=72, dtype=0)])
+def test_only_the_final_state_may_be_the_initial_one(kw):
+    """Also where o is as large as the states (bf16: 128 tokens with keys of 64)."""
+    L, p = linattn.lib(), _problem(**kw)
+    # q, k, v, g, h0, lengths, o, hT, workspace
+    a = _far(9)
+    a[6] = a[4]
+    assert L.ssd_linattn(ctypes.byref(p), *a, 1 << 40, None) == 9
