@@ -1,10 +1,12 @@
 """GPU tests of linear attention and rotary positions, beside those of test_gpu_linattn: refusals
-through the binding."""
+through the binding, and the decays' gradient within the spread of its roundings."""
 import pytest
 import torch
 
+import linattn_spread as spread
 import state_space_sequence_cumsum_amd as ssd
 from gpu_util import require_gpu
+from linattn_cases import ONE_CHUNK, SPREAD, inputs, one_chunk
 
 pytestmark = pytest.mark.gpu
 
@@ -24,3 +26,28 @@ def test_gradients_of_too_many_heads_are_refused(given):
     torch.cuda.synchronize()
     assert e.value.status == 3
     assert all((outs[n] == 3).all() for n in outs if n != "workspace")
+
+
+@pytest.mark.parametrize("rate", [0.3, 0.03])
+@pytest.mark.parametrize("case", SPREAD, ids=str)
+def test_the_decays_gradient_within_its_spread(case, rate):
+    dtype, b, L, G, H, dk, dv, state, lengths = case
+    dev = require_gpu()
+    d = inputs(case, dev, seed=60, rate=rate)
+    lt = None if lengths is None else torch.tensor(lengths, dtype=torch.int32, device=dev)
+    dg = ssd.ssd_linattn_backward(**d, scale=dk ** -0.5, lengths=lt)[3]
+    torch.cuda.synchronize()
+    parts, deviation = spread.decay_gradient(**d, scale=dk ** -0.5, lengths=lengths)
+    spread.check(dg, sum(parts.values()), deviation, "dg")
+
+
+@pytest.mark.parametrize("part", ONE_CHUNK)
+def test_one_chunks_decays_gradient_is_rounded_once(part):
+    """Scores and states that the decays' gradient is made of go in as two parts: of 2048 elements the
+    error is that of one rounding, 1 +- 0.02 (1.4 with either in one part)."""
+    dev = require_gpu()
+    d = one_chunk(part, dev, 61)
+    dg = ssd.ssd_linattn_backward(**d, scale=0.125)[3]
+    torch.cuda.synchronize()
+    parts, _ = spread.decay_gradient(**d, scale=0.125)
+    assert spread.one_rounding(dg, sum(parts.values())) < 1.1

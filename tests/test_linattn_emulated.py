@@ -9,6 +9,7 @@ import torch
 
 import kernel_emulator as emu
 import linattn_ref as ref
+import linattn_spread as spread
 import state_space_sequence_cumsum_amd as ssd
 
 TD = {"fp32": torch.float32, "bf16": torch.bfloat16}
@@ -115,6 +116,11 @@ def test_gradients(case):
         if name != "dh0":
             _unwritten([(r, e)], lengths)
         ref.check(x, r, e, name)
+    if decay == "token":
+        parts, deviation = spread.decay_gradient(**d, scale=dk ** -0.5, lengths=lengths)
+        value = sum(parts.values())
+        _unwritten([(value, deviation)], lengths)
+        spread.check(got[3], value, deviation, "dg within its spread")
 
 
 @pytest.mark.parametrize("case", [
