@@ -1,8 +1,10 @@
 """GPU tests of linear attention and rotary positions, beside those of test_gpu_linattn: refusals
-through the binding, and the decays' gradient within the spread of its roundings."""
+through the binding, the decays' gradient within the spread of its roundings, rotations whose
+last workgroup has fewer tokens."""
 import pytest
 import torch
 
+import linattn_ref as ref
 import linattn_spread as spread
 import state_space_sequence_cumsum_amd as ssd
 from gpu_util import require_gpu
@@ -51,3 +53,34 @@ def test_one_chunks_decays_gradient_is_rounded_once(part):
     torch.cuda.synchronize()
     parts, _ = spread.decay_gradient(**d, scale=0.125)
     assert spread.one_rounding(dg, sum(parts.values())) < 1.1
+
+
+@pytest.mark.parametrize("case", [
+    # dtype, b, L, heads, groups, width, rotated, interleaved, positions: tokens of a workgroup, of the last one
+    ("bf16", 1, 4099, 2, 1, 128, 128, False, "first"),      # 4, 3
+    ("bf16", 1, 9003, 2, 0, 64, 32, True, "first"),         # 8, 3
+    ("fp32", 3, 4777, 3, 1, 100, 36, True, "each"),         # 8, 3
+    ("bf16", 7, 2341, 2, 1, 24, 20, False, "each"),         # 8, 3 (single elements)
+    ("fp32", 1, 32783, 1, 1, 32, 32, False, "start"),       # 16, 15
+], ids=str)
+def test_rotations_whose_last_workgroup_is_not_full(case):
+    dtype, b, L, hq, hk, w, rot, inter, mode = case
+    dev = require_gpu()
+    gen = torch.Generator().manual_seed(L)
+    td = torch.float32 if dtype == "fp32" else torch.bfloat16
+    xs = [torch.randn(b, L, n, w, generator=gen).to(td).to(dev) for n in (hq, hk) if n]
+    t = torch.arange(L, dtype=torch.int32)
+    given = {"start": None, "first": torch.randint(0, 1 << 20, (b,), generator=gen, dtype=torch.int32),
+             "each": torch.randint(0, 1 << 20, (b, L), generator=gen, dtype=torch.int32)}[mode]
+    at = t.expand(b, L) if given is None else given[:, None] + t if mode == "first" else given
+    freqs = ssd.rotary_frequencies(rot, device=dev)
+    # outputs with the same bytes behind them afterwards
+    wide = [torch.full((x.numel() + 4096,), 7.0, device=dev, dtype=td) for x in xs]
+    outs = [t[:x.numel()].view(x.shape) for t, x in zip(wide, xs)]
+    ssd.ssd_rotary(xs[0], xs[1] if hk else None, freqs, None if given is None else given.to(dev),
+                   interleaved=inter, q_out=outs[0], k_out=outs[1] if hk else None)
+    torch.cuda.synchronize()
+    for x, y, whole in zip(xs, outs, wide):
+        r, e = ref.rotary(x, freqs, at, inter, False, 1.0)
+        ref.check(y, r, e, "rotated")
+        assert (whole[x.numel():] == 7).all()
