@@ -11,6 +11,9 @@
 // LDS, and then streams the heads of both arrays, 16 bytes of each side of the pairs a thread.
 // Bound by HBM (each element read and written once), or by launch latency for few tokens: 16384
 // tokens of 32 heads of 128 in 43 us (6.2 TB/s, the rate of a copy), one token of 128 sequences 3.3.
+// Where a side of the pairs, a head or a row is no whole number of 16 bytes, elements go one by one: the
+// same tokens of 32 heads of 80 in 27 us with all of it turned (16 bytes), in 99 with 24 elements in
+// halves of 12, in 67 with heads of 84 interleaved (bf16; 1.7 and 2.6 TB/s).
 #include <hip/hip_runtime.h>
 
 #include "ssd_device.h"
@@ -48,7 +51,6 @@ template <typename T, int V> struct Vec;
 template <> struct Vec<bf16, 8> { typedef bf16x8 t; };
 template <> struct Vec<float, 4> { typedef f32x4 t; };
 template <typename T> struct Vec<T, 1> { typedef T t; };
-template <typename T> struct Vec<T, 2> { typedef T t __attribute__((ext_vector_type(2))); };
 
 template <typename V> __device__ __forceinline__ float get(const V &v, int i)
 {
