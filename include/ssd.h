@@ -504,9 +504,11 @@ ssd_status ssd_linattn_step(const ssd_linattn_problem *problem, const void *q, c
  * added up), of a per-token g (dg [b, L, nheads], `dtype`; 0 where g is above 0 or minus
  * infinity; NULL: not wanted, and NULL it must be without SSD_DECAY_TOKEN) and of h0 (dh0 float32,
  * NULL: not wanted).  h0 and lengths are those of the forward call (NULL as there); its outputs
- * are not needed.  Rows of outputs behind a sequence's length are left as they were.  Beyond what
- * ssd_linattn_validate checks, nheads * key_dim <= 2^22 (the rows of all heads' dq and dk), else
- * SSD_ERR_UNSUPPORTED, and 0 bytes of workspace. */
+ * are not needed.  Rows of outputs behind a sequence's length are left as they were.  For SSD_BF16
+ * dq and dk are rounded once with a dg (scores and states in two bf16 parts), and have other last
+ * bits without one (in one part, as in ssd_linattn).  Beyond what ssd_linattn_validate checks,
+ * nheads * key_dim <= 2^22 (the rows of all heads' dq and dk), else SSD_ERR_UNSUPPORTED, and 0
+ * bytes of workspace. */
 size_t ssd_linattn_backward_workspace_bytes(const ssd_linattn_problem *problem);
 ssd_status ssd_linattn_backward(const ssd_linattn_problem *problem, const void *dout, const void *q,
                                 const void *k, const void *v, const void *g, const float *h0,

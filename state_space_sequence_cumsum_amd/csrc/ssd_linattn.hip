@@ -366,7 +366,10 @@ template <typename T, int DK, int NV> constexpr int waves_for()
     return DK == 128 ? 1 : 2;
 }
 
-// PARTS: bf16 parts of what is added to the state, 3, or 2 where the state only makes outputs.
+// PARTS: bf16 parts of what is added to the state, 3, or 2 where the state only makes outputs.  With
+// 3, 128 keys and 128 values one or two registers a lane are in scratch (none with 2); bf16 keys past 128
+// take more than 256 registers, accumulator registers among them, but for walks of 64 values
+// without a part in the decays' gradient.
 template <typename T, int DK, int NV, bool REV, Kind KIND, int PARTS>
 __global__ __launch_bounds__(kThreads, (waves_for<T, DK, NV>())) void walk_kernel(Walk a)
 {
@@ -375,7 +378,9 @@ __global__ __launch_bounds__(kThreads, (waves_for<T, DK, NV>())) void walk_kerne
     constexpr bool kOuts = KIND != kEnds, kParts = KIND == kDq || KIND == kDk;
     // Scores and the state that is read in two bf16 parts: the decays' gradient adds up their
     // products with both sides' rows, and with one part its error, 2.6e-3 of its size, was half as
-    // large again as that of its own rounding (1.7e-3; now below 2.3e-3).  2 % of the gradients' time.
+    // large again as that of its own rounding (1.7e-3; now 2.0e-3 to 2.5e-3, what is left being the
+    // states between the two walks, in one part).  dq and dk err by their own rounding alone, 1.7e-3;
+    // by 2.4e-3, with other bits, where no decays' gradient is wanted.  2 % of the gradients' time.
     constexpr bool kFine = kParts && sizeof(T) == 2;
     constexpr int CH = chunk_tokens<T, DK>(), NI = CH / 16, kTiles = NI * (NI + 1) / 2;
     constexpr int BV = 64 * NV;                                      // values
@@ -1013,10 +1018,12 @@ template <typename T, bool REV> hipError_t starts_go(const Walk &a, float *last,
 
 
 // How the chunks of a walk are split into segments, whose ends a first walk leaves.  `keys`: of the
-// widest state.  As many segments as workgroups fit at once: of 24 heads of 2 x 2048 tokens of 128 x 64
-// 384 take 44 us and 528, some of which wait for others, 52; 16384 tokens of 16 heads of 128 x 128 take
-// 126 us in 512 and 165 in 1024, 4096 of 4 heads of 256 x 256 60 in 256 and 90 in 512.  While each
-// has a CU to itself a segment may be one chunk; else it is two or more, as the chain over the
+// widest state.  As many as give each CU two workgroups, 512, or one where a walk leaves no room for
+// two (256).  More do not pay, though walks of 64 values fit three a CU: 24 heads of 2 x 2048 tokens
+// of 128 x 64 take 43 us in 384, 50 in 528 and 45 in 768, 16384 tokens of 16 heads of 128 x 128 113
+// in 512, 153 in 688 and 155 in 1024 (123 in 256; the same inputs again).  fp32 keys past 128 count as
+// one a CU; by their LDS two fit, and 8192 tokens of 8 heads of 256 x 256 take 329 us in 256, 289 in 512.
+// While each has a CU to itself a segment may be one chunk; else it is two or more, as the chain over the
 // segments is then the longer part (4 x 1024 tokens of 8 heads of 128 x 128: 37 us with two, 46 with one).
 // Segments are walked twice, and their ends and the chain are launches that take about the time of
 // two chunks (fp32: one), so there are none unless that is less than one walk over all: 256

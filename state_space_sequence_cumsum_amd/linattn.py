@@ -157,8 +157,8 @@ def ssd_linattn_backward(do, q, k, v, g=None, h0=None, dhT=None, *, scale=1.0, l
 
     Returns (dq, dk, dv, dg, dh0), each of its input's shape and type: dg None without a per-token
     g (fixed decays have no gradient here) or with want_dg False, dh0 None without an h0 or
-    with want_dh0 False.  Rows behind a sequence's length are left as they were in given
-    outputs and zeros in those allocated here."""
+    with want_dh0 False.  In bfloat16 dq and dk have other last bits without dg.  Rows behind a
+    sequence's length are left as they were in given outputs and zeros in those allocated here."""
     prob, dev, ptrs = _inputs(q, k, v, g, scale, 2)
     td, device = q.dtype, q.device
     dp, prob.do_pitch = _rows(do, "do", td, v.shape, dev, 2)
